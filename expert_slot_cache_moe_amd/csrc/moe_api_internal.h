@@ -1,5 +1,5 @@
 // Host-side internals shared by the C ABI's sources (moe_api.hip,
-// moe_layer.hip, moe_prefetch.hip): error reporting, the cache object, and
+// moe_layer.hip, moe_prefetch.hip, moe_operators.hip): error reporting, the cache object, and
 // the launch sequences several entry points share.  Not part of the ABI.
 #pragma once
 
@@ -59,6 +59,7 @@ hipError_t shared_sequence(const moe_shared_t *sh, int H, int Fs, const uint16_t
                            float *addend, uint8_t *ws, hipStream_t s);
 moe_status_t pool_view_of(const moe_pool_t *pool, PoolView &pv);
 moe_status_t check_shared(const moe_shared_t *sh, int H, int F, int *Fs);
+moe_status_t check_router(const moe_router_t *router, int32_t E, RouteParams &p);
 
 }  // namespace api
 }  // namespace moe

@@ -332,6 +332,52 @@ hipError_t launch_down_fused(const PoolView &pool, const int32_t *idx, const flo
 hipError_t launch_combine(const int32_t *idx, const float *w, int T, int K, int H, int num_rows,
                           const float *d, const float *addend, uint16_t *out, hipStream_t s);
 
+// Scored routing (k_route.hip): the router's fields, and ceil(log2 G) and
+// ceil(2^32 / (E / G)) for the kernel's index arithmetic.
+struct RouteParams {
+    int32_t score, num_groups, top_groups, group_score, renormalize;
+    float scale;
+    const float *bias;
+    int32_t log_groups;
+    uint32_t group_magic;
+};
+constexpr int kRouteMaxExperts = 2048, kRouteMaxGroups = 64;
+hipError_t launch_route(const RouteParams &p, int logits_type, const void *logits, int64_t stride, int T,
+                        int E, int K, int32_t *ids, float *w, hipStream_t s);
+
+// 4-bit rows (k_quant.hip).
+struct RowsParams {
+    int64_t rows;
+    int32_t cols;
+    int64_t stride;              // of the dense rows, in elements
+    const float *globals;        // E2M1, or NULL
+    int64_t rows_per_global;
+};
+hipError_t launch_quantize(int fmt, int type, const RowsParams &p, const void *src, uint8_t *codes,
+                           uint8_t *scales, hipStream_t s);
+hipError_t launch_dequantize(int fmt, int type, const RowsParams &p, const uint8_t *codes,
+                             const uint8_t *scales, void *dst, hipStream_t s);
+
+// MXFP4 products over pool rows (k_mx.hip).
+struct MxParams {
+    const uint8_t *codes, *scales;   // [P][n][k/2], [P][n][k/32]
+    int32_t P, n, k;
+    const uint16_t *x;               // bf16 [T], x_stride apart
+    int64_t x_stride;
+    const int32_t *idx;              // [R] or NULL (one matrix for every row)
+    int32_t T, K;                    // R = T K; route r reads x row r / K
+    int32_t swiglu;
+    int32_t out_type;
+    void *out;                       // [R][n or n / 2]
+    uint8_t *ws;
+};
+size_t mx_workspace_bytes(int P, int n, int k, int T, int K);
+constexpr int kMxMaxRows = 32768, kMxMaxRoutes = 131072, kMxMaxN = 1 << 20, kMxMaxK = 1 << 16;
+// The lists of routes by row depend on idx alone: a second product over the
+// same idx, T K and P may reuse those a first one left in the workspace
+// (reuse_lists, same T K and P), with its own T and K split.
+hipError_t launch_mx_product(const MxParams &p, bool reuse_lists, hipStream_t s);
+
 // The single-token layer step in two launches: stage 1 = miss gather
 // (+ the fetched experts' gate/up dots into gu [plan][2F]) | shared gate/up
 // | resident routes' gate/up; stage 2 = all down projections + combine.

@@ -5,11 +5,12 @@
 using namespace moe;
 using namespace moe::api;
 
-extern "C" {
+namespace {
 
-moe_status_t moe_layer_decode(moe_cache_t *c, int32_t layer, const void *x, const float *logits,
-                              int32_t T, int32_t K, const moe_shared_t *shared, int32_t max_fetch,
-                              void *out, int32_t *ids_out, float *w_out, void *stream) {
+// The layer step; with a router, its routes in the place of the top-k's.
+moe_status_t layer_decode(moe_cache_t *c, int32_t layer, const void *x, const float *logits, int32_t T,
+                          int32_t K, const moe_router_t *router, const moe_shared_t *shared,
+                          int32_t max_fetch, void *out, int32_t *ids_out, float *w_out, void *stream) {
     if (!c) return fail(MOE_INVALID_ARG, "NULL cache");
     if (c->nb == 0) return fail(MOE_INVALID_ARG, "cache has no weight banks");
     if (layer < 0 || layer >= c->d.num_layers)
@@ -27,6 +28,11 @@ moe_status_t moe_layer_decode(moe_cache_t *c, int32_t layer, const void *x, cons
         if (Fs > c->shared_ffn_cap)
             return fail(MOE_UNSUPPORTED, "shared ffn %d > the cache's workspace width %d", Fs, c->shared_ffn_cap);
     }
+    RouteParams rp{};
+    if (router) {
+        moe_status_t s = check_router(router, c->d.num_experts, rp);
+        if (s != MOE_OK) return s;
+    }
     hipStream_t s = static_cast<hipStream_t>(stream);
     int32_t *ids = ids_out ? ids_out : c->ws_ids;
     float *w = w_out ? w_out : c->ws_w;
@@ -35,8 +41,13 @@ moe_status_t moe_layer_decode(moe_cache_t *c, int32_t layer, const void *x, cons
     hipEvent_t *tev = timing ? &c->tev[(size_t)layer * 6] : nullptr;
 
     // Few token rows: the top-k runs inside the admission kernel.
-    const bool fused_topk =
-        T <= kFusedTopkRows && admit_fused_topk_supported(c->d.num_experts, c->d.num_slots, K);
+    const bool fused_topk = !router && T <= kFusedTopkRows &&
+                            admit_fused_topk_supported(c->d.num_experts, c->d.num_slots, K);
+    auto pick_routes = [&]() {
+        const int E = c->d.num_experts;
+        return router ? launch_route(rp, MOE_TYPE_F32, logits, E, T, E, K, ids, w, s)
+                      : launch_topk(logits, T, E, K, ids, w, s);
+    };
     if (c->d.overlap == 3 && shared && T > 0) {
         // The #678 split: the shared expert and its gate on the side stream,
         // forked here; top-k, admission, gather and the routed experts on the
@@ -55,7 +66,7 @@ moe_status_t moe_layer_decode(moe_cache_t *c, int32_t layer, const void *x, cons
         if (e != hipSuccess || re != hipSuccess)
             return joined(hip_fail(e != hipSuccess ? e : re, "shared expert on the side stream"));
         auto mark = [&](int i) { return timing ? record_timing(tev[i], s) : hipSuccess; };
-        if (!fused_topk && (e = launch_topk(logits, T, c->d.num_experts, K, ids, w, s)) != hipSuccess)
+        if (!fused_topk && (e = pick_routes()) != hipSuccess)
             return joined(hip_fail(e, "top-k launch"));
         if ((e = mark(0)) != hipSuccess) return joined(hip_fail(e, "timing"));
         moe_status_t st = fused_topk
@@ -76,7 +87,7 @@ moe_status_t moe_layer_decode(moe_cache_t *c, int32_t layer, const void *x, cons
         }
         return MOE_OK;
     }
-    if (!fused_topk) HIP_TRY(launch_topk(logits, T, c->d.num_experts, K, ids, w, s), "top-k launch");
+    if (!fused_topk) HIP_TRY(pick_routes(), "top-k launch");
     if (timing) HIP_TRY(record_timing(tev[0], s), "timing");
     moe_status_t st = fused_topk ? launch_admit_checked(c, layer, ids, R, max_fetch, s, c->ws_route_plan,
                                                         logits, T, K, w)
@@ -181,6 +192,23 @@ moe_status_t moe_layer_decode(moe_cache_t *c, int32_t layer, const void *x, cons
         c->trecorded[layer] = 1;
     }
     return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_layer_decode(moe_cache_t *c, int32_t layer, const void *x, const float *logits,
+                              int32_t T, int32_t K, const moe_shared_t *shared, int32_t max_fetch,
+                              void *out, int32_t *ids_out, float *w_out, void *stream) {
+    return layer_decode(c, layer, x, logits, T, K, nullptr, shared, max_fetch, out, ids_out, w_out, stream);
+}
+
+moe_status_t moe_layer_decode_router(moe_cache_t *c, int32_t layer, const void *x, const float *logits,
+                                     int32_t T, int32_t K, const moe_router_t *router,
+                                     const moe_shared_t *shared, int32_t max_fetch, void *out,
+                                     int32_t *ids_out, float *w_out, void *stream) {
+    return layer_decode(c, layer, x, logits, T, K, router, shared, max_fetch, out, ids_out, w_out, stream);
 }
 
 moe_status_t moe_cache_set_cpu_threads(moe_cache_t *c, int32_t threads) {

@@ -415,6 +415,148 @@ moe_status_t moe_prefetch(moe_cache_t *cache, int32_t layer, const int32_t *ids_
  * if one is pending (no-op otherwise). */
 moe_status_t moe_prefetch_join(moe_cache_t *cache, void *stream);
 
+/* ---------------------------------------------------------------- scored routing */
+
+/* A router that scores, biases and groups its experts. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+/* Element types of dense rows. */
+enum { MOE_TYPE_F32 = 0, MOE_TYPE_BF16 = 1 };
+typedef struct {
+    int32_t score;            /* MOE_SCORE_*: s = softmax(logits) or 1 / (1 + exp(-logit)) */
+    int32_t num_groups;       /* G >= 1, divides E: group g holds experts
+                                 [g E / G, (g + 1) E / G); at most 64           */
+    int32_t top_groups;       /* groups a row may pick from, 1..G               */
+    int32_t group_score;      /* MOE_GROUP_MAX: a group's largest c; MOE_GROUP_TOP2:
+                                 the sum of its two largest                     */
+    int32_t renormalize;      /* 1: weights divided by their sum over the picks */
+    float scale;              /* multiplies every weight                        */
+    const float *bias_dev;    /* fp32 [E], added to the scores for the choice only;
+                                 or NULL                                        */
+} moe_router_t;
+
+/* Scored top-K routing.  logits_dev: [T] rows of E logits of logits_type
+ * (MOE_TYPE_*), row_stride elements apart (>= E).  With s_e the score of
+ * expert e over the row's available experts and c_e = s_e + bias_e:
+ *  - an expert is available unless its logit is NaN or -infinity, or its
+ *    c_e is (logits of +infinity share a softmax evenly);
+ *  - the top_groups groups of largest value, ties to the lower group, stay:
+ *    the value is the largest c of the group's available experts, or the
+ *    sum of the two largest (the largest alone, if it is the only one);
+ *  - of their available experts the K of largest c are picked, largest
+ *    first, ties to the lower id; without a bias experts are ordered by
+ *    their logits (scores are increasing in them), and so are groups under
+ *    MOE_GROUP_MAX;
+ *  - the weight of a pick is scale * s_e, or scale * s_e / (sum of the
+ *    picks' s) with renormalize (evenly, if that sum is 0).
+ * Scores and their order are computed in 64 bits, so the picks do not
+ * depend on the rounding of near scores; weights are rounded once, to
+ * fp32.  Where fewer than K experts can be picked (masked rows), the rest
+ * get id -1 and weight 0: such a route adds nothing in the later steps.
+ * ids_dev: int32 [T][K]; w_dev: fp32 [T][K].  Asynchronous, capturable.
+ * Errors: MOE_INVALID_ARG (T < 0, K < 1, K > E, K > 64, bad router fields,
+ * a stride below E, null pointers), MOE_UNSUPPORTED (E > 2048, more than
+ * 64 groups). */
+moe_status_t moe_route(const moe_router_t *router, int32_t logits_type, const void *logits_dev,
+                       int64_t row_stride, int32_t T, int32_t E, int32_t K, int32_t *ids_dev,
+                       float *w_dev, void *stream);
+
+/* moe_layer_decode with the routes of moe_route (fp32 logits [T][E],
+ * contiguous) in the place of moe_topk's: a route of id -1 counts as
+ * invalid in the statistics and adds nothing.  router NULL is
+ * moe_layer_decode itself.  Errors: as moe_route and moe_layer_decode. */
+moe_status_t moe_layer_decode_router(moe_cache_t *cache, int32_t layer, const void *x_dev,
+                                     const float *logits_dev, int32_t T, int32_t K,
+                                     const moe_router_t *router, const moe_shared_t *shared,
+                                     int32_t max_fetch, void *out_dev, int32_t *ids_out_dev,
+                                     float *w_out_dev, void *stream);
+
+/* ---------------------------------------------------------------- 4-bit rows */
+
+/* Rows of floats to a 4-bit format (MOE_FMT_MXFP4 or MOE_FMT_E2M1), the
+ * layout of that format's banks.  src_dev: [rows] rows of cols elements of
+ * src_type, src_stride elements apart (>= cols); codes_dev: [rows][cols/2];
+ * scales_dev: [rows][cols/B], B = 32 (MXFP4) or 16 (E2M1).  Of each block
+ * of B consecutive elements with largest magnitude a:
+ *  - MXFP4: the scale is 2^(floor(log2 a) - 2), at least 2^-127 (a = 0 too);
+ *  - E2M1: the scale is a / (6 g) rounded to the nearest E4M3 value, ties
+ *    to even, at most 448; g is the row's global scale, globals_dev[row /
+ *    rows_per_global] (fp32), or 1 with globals_dev NULL;
+ *  - each code is the E2M1 value nearest to x / (scale g), ties to the even
+ *    code, saturating at 6, with the sign of x (zeros too); all zeros where
+ *    the scale is 0.
+ * The result is that of exact arithmetic: no border is moved by rounding.
+ * A block holding NaN or infinity, or (E2M1) whose g is not a positive
+ * finite number, gets the format's NaN scale (0xFF, 0x7F) and zero codes.
+ * Asynchronous, capturable.  Errors: MOE_INVALID_ARG (another format or
+ * type, rows < 0, cols < 1 or not a multiple of B, a stride below cols,
+ * rows_per_global < 1 with globals, null or misaligned pointers: src to
+ * its element, codes to 8 bytes (MXFP4: 16), globals to 4). */
+moe_status_t moe_quantize_rows(int32_t weight_format, int32_t src_type, const void *src_dev,
+                               int64_t src_stride, int64_t rows, int32_t cols,
+                               const float *globals_dev, int64_t rows_per_global, void *codes_dev,
+                               void *scales_dev, void *stream);
+
+/* The values 4-bit rows stand for, code * scale * g, rounded once to
+ * dst_type; a NaN scale gives NaN.  dst_dev: [rows] rows of cols, dst_stride
+ * elements apart; the gaps between rows are not written.  Other arguments
+ * and errors as moe_quantize_rows. */
+moe_status_t moe_dequantize_rows(int32_t weight_format, const void *codes_dev, const void *scales_dev,
+                                 int64_t rows, int32_t cols, const float *globals_dev,
+                                 int64_t rows_per_global, int32_t dst_type, void *dst_dev,
+                                 int64_t dst_stride, void *stream);
+
+/* ---------------------------------------------------------------- MXFP4 products */
+
+/* MXFP4 matrices [n][k] of the rows of one pool bank pair. */
+typedef struct {
+    int32_t num_rows;         /* matrices, 1..32768                             */
+    int32_t n, k;             /* k a multiple of 32                             */
+    const void *codes_dev;    /* [num_rows][n][k/2], 16-byte aligned            */
+    const void *scales_dev;   /* [num_rows][n][k/32]                            */
+} moe_mx_bank_t;
+
+/* Bytes of device workspace moe_mx_product needs (0 for sizes it refuses). */
+int64_t moe_mx_product_workspace_bytes(int32_t num_rows, int32_t n, int32_t k, int32_t T, int32_t K);
+
+/* The product over pool rows with both operands in MXFP4, on the scaled
+ * 4-bit matrix instructions.  For each route r = t K + j, row i = idx[t][j]:
+ *   y[r] = W_i q(x_t),  q = the MXFP4 quantisation of moe_quantize_rows;
+ *   out[r] = y[r], or with swiglu (n even) silu(y[r][:n/2]) * y[r][n/2:]
+ * summed in fp32, rounded once to out_type.  x_dev: bf16 [T] rows of k,
+ * x_stride elements apart; idx_dev: int32 [T][K], or NULL with num_rows =
+ * K = 1 (every row takes the one matrix); out_dev: [T K][n or n/2].  A
+ * route whose id is outside [0, num_rows) gets a row of zeros.  A NaN scale
+ * or a block of x with NaN or infinity makes the outputs that read it NaN.
+ * A route's result depends on its row's bytes and its x alone.
+ * workspace_dev: moe_mx_product_workspace_bytes(...), 256-byte aligned,
+ * overwritten; calls that share it must be ordered.  Asynchronous,
+ * capturable.  Errors: MOE_INVALID_ARG (sizes, strides, null or misaligned
+ * pointers, workspace too small), MOE_UNSUPPORTED (num_rows > 32768, T K >
+ * 131072, K > 64, n > 2^20, k > 2^16). */
+moe_status_t moe_mx_product(const moe_mx_bank_t *bank, const void *x_dev, int64_t x_stride,
+                            const int32_t *idx_dev, int32_t T, int32_t K, int32_t swiglu,
+                            int32_t out_type, void *out_dev, void *workspace_dev,
+                            int64_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace moe_routed_decode_mx needs (0 for sizes it
+ * refuses). */
+int64_t moe_routed_mx_workspace_bytes(int32_t num_rows, int32_t hidden, int32_t ffn, int32_t T, int32_t K);
+
+/* moe_routed_decode over an MXFP4 pool with 4-bit activations: the gate/up
+ * product with SwiGLU (its result rounded to bf16), the down product (fp32),
+ * and the combine
+ *   out[t] = bf16( sum over k ascending with a valid row of w[t][k] y[t][k]
+ *                  + addend[t] ).
+ * Results differ from moe_routed_decode's by the quantisation of x and of
+ * the activation.  Arguments as moe_routed_decode, x 16-byte aligned.
+ * Errors: as moe_mx_product; MOE_INVALID_ARG for another format;
+ * MOE_UNSUPPORTED (hidden or ffn not a multiple of 32, T > 65535). */
+moe_status_t moe_routed_decode_mx(const moe_pool_t *pool, const void *x_dev, const int32_t *idx_dev,
+                                  const float *w_dev, int32_t T, int32_t K, const float *addend_dev,
+                                  void *out_dev, void *workspace_dev, int64_t workspace_bytes,
+                                  void *stream);
+
 /* ---------------------------------------------------------------- inspection */
 
 /* Copies the layer's statistics (layer = -1: sums over layers) into
