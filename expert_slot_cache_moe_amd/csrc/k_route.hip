@@ -6,13 +6,15 @@
 // lower index, and two scores that differ by less than an fp32 rounding are
 // still two scores: they are computed and compared in 64 bits.
 //
-// A lane holds experts lane, lane + 64, ... of the row.  A choice value is
-// kept as a 64-bit integer whose unsigned order is the order of the values
-// (0: not available), split into its halves: a selection round takes the
-// wave's maximum of the upper halves alone (DPP max steps) and looks at the
-// lower halves and the index only where two candidates share it.  Lane k
-// keeps pick k and recomputes its score at the end, so no score is carried
-// through the rounds.
+// A lane holds experts lane, lane + 64, ... of the row.  Choice values are
+// first formed in fp32, where their error is bounded; the K-th largest of
+// the 64 lanes' own maxima, less that bound, is a floor that every pick
+// reaches and few others do (measured: 11 to 12 candidates for 10 picks of
+// 512).  The candidates are packed one to a lane, their values computed in
+// 64 bits, and their ranks counted.  Where more than 64 values reach the
+// floor (rows of equal scores), or two groups at the border of the choice
+// are closer than the bound, the row takes the long way: every value in 64
+// bits, K rounds of a wave maximum.
 #include "moe_internal.h"
 
 namespace moe {
@@ -27,17 +29,6 @@ __device__ __forceinline__ uint64_t order_key(double v) {
 }
 __device__ __forceinline__ double key_value(uint64_t k) {
     return __longlong_as_double((long long)(k ^ ((k >> 63) ? 0x8000000000000000ull : ~0ull)));
-}
-
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int off = kWave / 2; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
-    return v;
-}
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int off = kWave / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
-    return v;
 }
 
 __device__ __forceinline__ float load_logit(const float *p) { return *p; }
@@ -58,102 +49,126 @@ __device__ __forceinline__ void merge_top2(uint64_t &a, uint64_t &b, uint64_t oa
     b = b < lo ? lo : b;
 }
 
-template <int VPL, typename L>
-__global__ __launch_bounds__(kRowsPerBlock *kWave) void route_kernel(
-    const L *__restrict__ logits, int64_t stride, int T, int E, int K, RouteParams p,
-    int32_t *__restrict__ ids, float *__restrict__ w) {
-    extern __shared__ __align__(16) uint64_t keys_lds[];   // [rows per block][E], groups only
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int row = blockIdx.x * kRowsPerBlock + wave;
-    if (row >= T) return;
-    const L *lr = logits + (int64_t)row * stride;
-
-    float v[VPL];
-    float top = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-        const int e = lane + kWave * j;
-        const float l = e < E ? load_logit(lr + e) : -INFINITY;
-        v[j] = l != l ? -INFINITY : l;
-        top = fmaxf(top, v[j]);
+// Sum over the wave, to every lane, in a fixed order (DPP moves of the halves).
+__device__ __forceinline__ double wave_total(double v) {
+#define MOE_ADD_STEP(CTRL, RM)                                                                        \
+    {                                                                                                 \
+        const uint64_t u = (uint64_t)__double_as_longlong(v);                                         \
+        const uint32_t l = dpp_or_zero<CTRL, RM>((uint32_t)u), h = dpp_or_zero<CTRL, RM>((uint32_t)(u >> 32)); \
+        v += __longlong_as_double((long long)(((uint64_t)h << 32) | l));                              \
     }
-    // Scores are needed for every expert where the choice adds a bias or
-    // sums two of a group; a plain softmax weight needs their sum too.
-    const bool softmax = p.score == MOE_SCORE_SOFTMAX;
-    const bool score_keys = p.bias != nullptr || (p.num_groups > 1 && p.group_score == MOE_GROUP_TOP2);
-    double z = 1.0;
-    if (softmax) {
-        top = wave_max(top);
-        if (score_keys || !p.renormalize) {
-            double part = 0.0;
-#pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (v[j] > -INFINITY) part += shifted_exp(v[j], top);
-            z = wave_sum(part);
-        }
-    }
-    auto score_of = [&](float l) { return softmax ? shifted_exp(l, top) / z : sigmoid(l); };
+    MOE_ADD_STEP(kDppRowShr1, 0xf)
+    MOE_ADD_STEP(kDppRowShr2, 0xf)
+    MOE_ADD_STEP(kDppRowShr4, 0xf)
+    MOE_ADD_STEP(kDppRowShr8, 0xf)
+    MOE_ADD_STEP(kDppRowBcast15, 0xa)
+    MOE_ADD_STEP(kDppRowBcast31, 0xc)
+#undef MOE_ADD_STEP
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const uint32_t l = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, kWave - 1);
+    const uint32_t h = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), kWave - 1);
+    return __longlong_as_double((long long)(((uint64_t)h << 32) | l));
+}
 
-    // choice keys; with groups ranked by score sums and no bias, the group
-    // keys (scores) differ from the choice keys (logits)
+// Largest of v over the wave, to every lane.
+__device__ __forceinline__ float wave_max_f32(float v) {
+#define MOE_MAX_STEP(CTRL, RM)                                                                              \
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), CTRL, RM, \
+                                                            0xf, false)));
+    MOE_MAX_STEP(kDppRowShr1, 0xf)
+    MOE_MAX_STEP(kDppRowShr2, 0xf)
+    MOE_MAX_STEP(kDppRowShr4, 0xf)
+    MOE_MAX_STEP(kDppRowShr8, 0xf)
+    MOE_MAX_STEP(kDppRowBcast15, 0xa)
+    MOE_MAX_STEP(kDppRowBcast31, 0xc)
+#undef MOE_MAX_STEP
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), kWave - 1));
+}
+
+// What one row needs, in registers and in the wave's LDS.
+template <int VPL> struct RowState {
+    float v[VPL];         // logits, -infinity where there is none
+    float top;            // softmax: the largest
+    double z;             // softmax: sum of exp(l - top), or 1 where it is not needed
+    const RouteParams &p;
+    __device__ __forceinline__ double score(float l) const {
+        return p.score == MOE_SCORE_SOFTMAX ? shifted_exp(l, top) / z : sigmoid(l);
+    }
+    // what experts are picked by; -infinity: not available
+    __device__ __forceinline__ double choice(float l, int e) const {
+        if (!(l > -INFINITY)) return -INFINITY;
+        const double c = p.bias != nullptr ? score(l) + (double)p.bias[e] : (double)l;
+        return c > -INFINITY ? c : -INFINITY;   // NaN too
+    }
+};
+
+struct Candidate {
+    float l;
+    int32_t e;
+};
+// The floor may let through this many lanes more than K, and is looked for
+// by at most so many halvings.
+constexpr int kSpare = 4, kHalvings = 10;
+
+// The wave's lanes g * lanes .. of group g; every group's place among the
+// groups, by `before`.
+template <typename V> __device__ __forceinline__ uint64_t kept_groups(const RouteParams &p, int lane, V value, V none) {
+    const int lanes = kWave >> p.log_groups, g = lane / lanes;
+    int before = 0;
+    for (int og = 0; og < p.num_groups; ++og) {
+        const V ov = __shfl(value, og * lanes, kWave);
+        before += ov > value || (ov == value && og < g);
+    }
+    return __ballot(g < p.num_groups && value != none && before < p.top_groups);
+}
+
+// e / (E / G) by multiplication.
+__device__ __forceinline__ int group_of(const RouteParams &p, int gs, int e) {
+    return gs == 1 ? e : (int)__umulhi((uint32_t)e, p.group_magic);
+}
+
+__device__ __forceinline__ void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// The long way: every choice value in 64 bits, as integers of the same
+// order (0: not available), K rounds of a maximum of their upper halves.
+// Returns lane k's pick k, or -1.
+template <int VPL>
+__device__ __forceinline__ int pick_long_way(const RowState<VPL> &row, const RouteParams &p, int E, int K,
+                                                       int lane, uint64_t *gk) {
     uint32_t hi[VPL], lo[VPL];
-    uint64_t *gk = keys_lds + (size_t)wave * E;
+    const bool score_sums = p.num_groups > 1 && p.group_score == MOE_GROUP_TOP2 && p.bias == nullptr;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
         const int e = lane + kWave * j;
-        uint64_t key = 0, gkey = 0;
-        if (v[j] > -INFINITY) {
-            double c = (double)v[j];
-            if (score_keys) {
-                const double s = score_of(v[j]);
-                gkey = order_key(s);
-                if (p.bias != nullptr) {
-                    c = s + (double)p.bias[e];
-                    gkey = c > -INFINITY ? order_key(c) : 0;
-                }
-            }
-            key = c > -INFINITY ? order_key(c) : 0;
-            if (!score_keys) gkey = key;
-        }
-        if (p.num_groups > 1 && e < E) gk[e] = gkey;
+        const double c = e < E ? row.choice(row.v[j], e) : -INFINITY;
+        const uint64_t key = c > -INFINITY ? order_key(c) : 0;
+        if (p.num_groups > 1 && e < E) gk[e] = key != 0 && score_sums ? order_key(row.score(row.v[j])) : key;
         hi[j] = (uint32_t)(key >> 32);
         lo[j] = (uint32_t)key;
     }
-
     if (p.num_groups > 1) {
-        // 64 / 2^ceil(log2 G) lanes scan each group, then pair up
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_sync();
         const int G = p.num_groups, gs = E / G;
-        const int lanes = kWave >> p.log_groups;
-        const int g = lane / lanes, sub = lane & (lanes - 1);
+        const int lanes = kWave >> p.log_groups, g = lane / lanes;
         uint64_t a = 0, b = 0;
         if (g < G)
-            for (int i = sub; i < gs; i += lanes) {
-                const uint64_t k = gk[g * gs + i];
-                merge_top2(a, b, k, 0);
-            }
+            for (int i = lane & (lanes - 1); i < gs; i += lanes) merge_top2(a, b, gk[g * gs + i], (uint64_t)0);
         for (int off = 1; off < lanes; off <<= 1) {
             const uint64_t oa = __shfl_xor(a, off, kWave), ob = __shfl_xor(b, off, kWave);
             merge_top2(a, b, oa, ob);
         }
         uint64_t value = a;
         if (p.group_score == MOE_GROUP_TOP2 && b != 0) value = order_key(key_value(a) + key_value(b));
-        // how many groups come before this one: larger, or equal and lower
-        int before = 0;
-        for (int og = 0; og < G; ++og) {
-            const uint64_t ov = __shfl(value, og * lanes, kWave);
-            before += ov > value || (ov == value && og < g);
-        }
-        const uint64_t kept = __ballot(g < G && value != 0 && before < p.top_groups);
+        const uint64_t kept = kept_groups<uint64_t>(p, lane, value, 0);
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             const int e = lane + kWave * j;
-            const int eg = gs == 1 ? e : (int)__umulhi((uint32_t)e, p.group_magic);   // e / gs
-            if (e < E && !((kept >> (eg * lanes)) & 1)) hi[j] = lo[j] = 0;
+            if (e < E && !((kept >> (group_of(p, gs, e) * lanes)) & 1)) hi[j] = lo[j] = 0;
         }
     }
-
     int mine = -1;
     for (int k = 0; k < K; ++k) {
         uint32_t best = 0;
@@ -161,45 +176,206 @@ __global__ __launch_bounds__(kRowsPerBlock *kWave) void route_kernel(
         for (int j = 0; j < VPL; ++j) best = max(best, hi[j]);
         const uint32_t m = wave_max_u32(best);
         if (m == 0) break;
-        int at = -1, n = 0;
+        // among equal upper halves the larger lower half, then the lower index
+        uint64_t t = 0;
 #pragma unroll
-        for (int j = VPL - 1; j >= 0; --j)
+        for (int j = 0; j < VPL; ++j)
             if (hi[j] == m) {
-                at = j;
-                ++n;
+                const uint64_t c = ((uint64_t)lo[j] << 32) | (uint32_t)~(lane + kWave * j);
+                t = c > t ? c : t;
             }
-        const uint64_t who = __ballot(n > 0);
-        int e;
-        if (__popcll(who) == 1 && __ballot(n > 1) == 0) {
-            e = __builtin_amdgcn_readlane(lane + kWave * at, __ffsll((unsigned long long)who) - 1);
-        } else {
-            // equal upper halves: the larger lower half, then the lower index
-            uint64_t t = 0;
-#pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (hi[j] == m) {
-                    const uint64_t c = ((uint64_t)lo[j] << 32) | (uint32_t)~(lane + kWave * j);
-                    t = c > t ? c : t;
-                }
-            t = wave_max_u64(t);
-            e = (int)~(uint32_t)t;
-        }
+        const int e = (int)~(uint32_t)wave_max_u64(t);
 #pragma unroll
         for (int j = 0; j < VPL; ++j)
             if (lane + kWave * j == e) hi[j] = 0;
         if (lane == k) mine = e;
     }
+    return mine;
+}
 
-    double s = 0.0;
-    if (mine >= 0) s = score_of(load_logit(lr + mine));
-    if (p.renormalize) {
-        const double total = wave_sum(s);
-        const int n = __popcll(__ballot(mine >= 0));
-        s = total > 0.0 ? s / total : (mine >= 0 ? 1.0 / n : 0.0);
+template <int VPL, typename L>
+__global__ __launch_bounds__(kRowsPerBlock *kWave) void route_kernel(
+    const L *__restrict__ logits, int64_t stride, int T, int E, int K, RouteParams p,
+    int32_t *__restrict__ ids, float *__restrict__ w) {
+    extern __shared__ __align__(16) uint64_t lds[];   // [rows per block][E], groups only
+    __shared__ Candidate cand[kRowsPerBlock][kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int row_i = blockIdx.x * kRowsPerBlock + wave;
+    if (row_i >= T) return;
+    const L *lr = logits + (int64_t)row_i * stride;
+
+    RowState<VPL> row{{}, -INFINITY, 1.0, p};
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+        const int e = lane + kWave * j;
+        const float l = e < E ? load_logit(lr + e) : -INFINITY;
+        row.v[j] = l != l ? -INFINITY : l;
+        row.top = fmaxf(row.top, row.v[j]);
     }
-    if (lane < K) {
-        ids[(int64_t)row * K + lane] = mine;
-        w[(int64_t)row * K + lane] = (float)(s * (double)p.scale);
+    const bool softmax = p.score == MOE_SCORE_SOFTMAX, biased = p.bias != nullptr;
+    const bool top2 = p.num_groups > 1 && p.group_score == MOE_GROUP_TOP2;
+    if (softmax) {
+        row.top = wave_max_f32(row.top);
+        // a renormalised softmax weight needs no sum over the row, and
+        // neither does the order without a bias
+        if (biased || !p.renormalize) {
+            double part = 0.0;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (row.v[j] > -INFINITY) part += shifted_exp(row.v[j], row.top);
+            row.z = wave_total(part);
+        }
+    }
+
+    // Choice values in fp32.  exp and the reciprocal are good to a few ulp,
+    // and an error d in their argument l shows as |l| s (1 - s) 2^-24 in the
+    // score: scores are within 2^-21, their sums with a bias within 2^-21 +
+    // 2^-24 |c|.  Two values further apart than slack(c) are in true order.
+    auto slack = [](float c) { return (1.f + fabsf(c)) * 0x1p-19f; };
+    const float rz = (float)(1.0 / row.z);
+    auto score32 = [&](float l) {
+        if (softmax) return l == row.top ? rz : expf(l - row.top) * rz;
+        return __builtin_amdgcn_rcpf(1.f + __expf(-l));
+    };
+    float c[VPL], gv[VPL];   // choice and, for the groups, what their value is made of
+    float best = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+        const int e = lane + kWave * j;
+        const bool on = row.v[j] > -INFINITY;
+        float s = 0.f;
+        if (biased || top2) s = score32(row.v[j]);
+        c[j] = row.v[j];
+        if (biased) c[j] = s + (e < E ? p.bias[e] : 0.f);
+        c[j] = on && c[j] > -INFINITY ? c[j] : -INFINITY;
+        gv[j] = top2 && !biased && on ? s : c[j];
+    }
+
+    bool settled = true;
+    if (p.num_groups > 1) {
+        float *gl = reinterpret_cast<float *>(lds + (size_t)wave * E);
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            if (lane + kWave * j < E) gl[lane + kWave * j] = gv[j];
+        wave_lds_sync();
+        const int G = p.num_groups, gs = E / G;
+        const int lanes = kWave >> p.log_groups, g = lane / lanes;
+        float a = -INFINITY, b = -INFINITY;
+        auto merge = [&](float oa, float ob) {
+            const float lo = fminf(a, oa);
+            a = fmaxf(a, oa);
+            b = fmaxf(fmaxf(b, ob), lo);
+        };
+        if (g < G)
+            for (int i = lane & (lanes - 1); i < gs; i += lanes) merge(gl[g * gs + i], -INFINITY);
+        for (int off = 1; off < lanes; off <<= 1) {
+            const float oa = __shfl_xor(a, off, kWave), ob = __shfl_xor(b, off, kWave);
+            merge(oa, ob);
+        }
+        const float value = top2 && b > -INFINITY ? a + b : a;
+        const uint64_t kept = kept_groups<float>(p, lane, value, -INFINITY);
+        if (biased || top2) {
+            // the kept and the dropped must be further apart than their errors
+            const bool in = (kept >> lane) & 1;
+            const float err = slack(a) + (top2 && b > -INFINITY ? slack(b) : 0.f);
+            const float under = err < INFINITY ? value - err : -INFINITY, over = err < INFINITY ? value + err : INFINITY;
+            const float worst = -wave_max_f32(in ? -under : -INFINITY);
+            const float next = wave_max_f32(g < G && !in && value > -INFINITY ? over : -INFINITY);
+            settled = worst > next || !(next > -INFINITY);
+        }
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const int e = lane + kWave * j;
+            if (e < E && !((kept >> (group_of(p, gs, e) * lanes)) & 1)) c[j] = -INFINITY;
+        }
+        wave_lds_sync();   // the long way writes the same LDS
+    }
+
+    // The floor: a value that at least K, and not many more, of the lanes'
+    // maxima reach -- found by halving the range between their least and
+    // largest, or, where that has not narrowed it (maxima many magnitudes
+    // apart), as the K-th largest maximum itself.
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) best = fmaxf(best, c[j]);
+    float low = -INFINITY;
+    if (VPL > 1 && __popcll(__ballot(best > -INFINITY)) > K + kSpare) {
+        float under = -wave_max_f32(best > -INFINITY ? -best : -INFINITY), over = wave_max_f32(best);
+        int n = kWave;
+        for (int i = 0; i < kHalvings && n > K + kSpare; ++i) {
+            const float mid = 0.5f * under + 0.5f * over;
+            const int m = __popcll(__ballot(best >= mid));
+            if (m >= K) {
+                under = mid;
+                n = m;
+            } else {
+                over = mid;
+            }
+        }
+        low = under;
+        if (n > kWave / 2) {
+            n = 0;
+            while (n < K) {
+                low = wave_max_f32(best);
+                const bool is = best == low;
+                n += __popcll(__ballot(is));
+                if (is) best = -INFINITY;
+            }
+        }
+        if (biased) low -= slack(low);
+        if (!(low > -INFINITY)) low = -INFINITY;   // also where it is NaN: infinity less infinity
+    }
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+        const bool in = c[j] > -INFINITY && c[j] >= low;
+        const uint64_t m = __ballot(in);
+        const int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
+        if (in && at < kWave) cand[wave][at] = Candidate{row.v[j], lane + kWave * j};
+        n += __popcll(m);
+    }
+    settled = settled && n <= kWave;
+
+    int rank = lane;      // the place of this lane's pick
+    Candidate my{-INFINITY, -1};
+    double s = 0.0;       // its score
+    if (settled) {
+        wave_lds_sync();
+        if (lane < n) my = cand[wave][lane];
+        // candidates lie in index order: of equal values the lower lane is first
+        rank = 0;
+        if (biased) {
+            s = row.score(my.l);
+            const double mine = lane < n ? s + (double)p.bias[my.e] : -INFINITY;
+            const uint64_t key = order_key(mine);
+            for (int i = 0; i < n; ++i) {
+                const uint64_t ok =
+                    ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(key >> 32), i) << 32) |
+                    (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)key, i);
+                rank += ok > key || (ok == key && i < lane);
+            }
+        } else {
+            for (int i = 0; i < n; ++i) {
+                const float ol = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my.l), i));
+                rank += ol > my.l || (ol == my.l && i < lane);
+            }
+            s = row.score(my.l);
+        }
+        if (lane >= n) rank = lane;   // behind the candidates
+    } else {
+        my.e = pick_long_way<VPL>(row, p, E, K, lane, lds + (size_t)wave * E);
+        if (my.e >= 0) s = row.score(load_logit(lr + my.e));
+    }
+
+    const bool picked = my.e >= 0 && rank < K;
+    if (!picked) s = 0.0;
+    if (p.renormalize) {
+        const double total = wave_total(s);
+        const int count = __popcll(__ballot(picked));
+        s = total > 0.0 ? s / total : (picked ? 1.0 / count : 0.0);
+    }
+    if (rank < K) {
+        ids[(int64_t)row_i * K + rank] = picked ? my.e : -1;
+        w[(int64_t)row_i * K + rank] = (float)(s * (double)p.scale);
     }
 }
 

@@ -137,6 +137,23 @@ def test_route_orders_scores_closer_than_an_fp32_rounding():
                  top2=True)
 
 
+@pytest.mark.parametrize("E,groups,top_groups,top2", [(64, 1, 1, False), (256, 1, 1, False), (256, 8, 3, True),
+                                                      (256, 8, 3, False), (1024, 16, 5, True)])
+def test_route_under_biases_of_every_size(E, groups, top_groups, top2):
+    g = W.rng(4, "biases", E, groups, top2)
+    x = g.standard_normal((24, E)).astype(np.float32)
+    x[1::4] = np.round(x[1::4] * 2) / 2                       # many equal scores
+    x[2::4] = x[2::4, :1]
+    inf, low = np.inf, np.finfo(np.float32).min
+    for b in (np.zeros(E), np.where(np.arange(E) % 3 == 0, 1e6, -1e6), np.where(g.random(E) < 0.5, low, 0.0),
+              np.where(g.random(E) < 0.02, inf, 0.1), g.standard_normal(E) * 1e-8, g.standard_normal(E) * 1e3,
+              np.where(g.random(E) < 0.9, -inf, 0.0)):
+        bias = torch.from_numpy(b.astype(np.float32)).cuda()
+        for score in ("sigmoid", "softmax"):
+            _check_route(torch.from_numpy(x).cuda(), 7, bias=bias, score=score, groups=groups, top_groups=top_groups,
+                         top2=top2)
+
+
 def test_route_of_strided_rows_leaves_the_rest_alone():
     g = W.rng(5, "strided")
     T, E, K = 37, 50, 4
