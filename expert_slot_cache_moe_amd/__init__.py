@@ -416,45 +416,66 @@ def moe_prefetch_join(cache: Cache, stream=None) -> None:
 
 # ---------------------------------------------------------------- scored routing, 4-bit rows, MXFP4 products
 
-# torch element types of dense rows (bf16 also as its 16-bit patterns)
-_TYPES = {"torch.float32": MOE_TYPE_F32, "torch.bfloat16": MOE_TYPE_BF16, "torch.int16": MOE_TYPE_BF16,
-          "torch.uint16": MOE_TYPE_BF16}
+# These calls are short, so their checks are kept to a few attribute reads.
+
+_torch = None
+_TYPES: dict = {}
+_I32 = _F32 = _U8 = None
+
+
+def _load_torch():
+    """torch and the element types of dense rows, looked up once."""
+    global _torch, _I32, _F32, _U8
+    import torch
+
+    # bf16 also as its 16-bit patterns
+    _TYPES.update({torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16, torch.int16: MOE_TYPE_BF16,
+                   torch.uint16: MOE_TYPE_BF16})
+    _I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
+    _torch = torch
 
 
 def _type_of(t, what):
-    try:
-        return _TYPES[str(t.dtype)]
-    except KeyError:
-        raise ValueError(f"{what}: expected float32 or bfloat16 (or bf16 bits as int16), got {t.dtype}") from None
+    v = _TYPES.get(t.dtype)
+    if v is None:
+        raise ValueError(f"{what}: expected float32 or bfloat16 (or bf16 bits as int16), got {t.dtype}")
+    return v
 
 
 def _on_current_device(*tensors):
-    """The library launches on the current device: every tensor must be on it."""
-    import torch
-
-    dev = torch.cuda.current_device()
+    """The library launches on the current device: every tensor must be on it.  Returns its index."""
+    if _torch is None:
+        _load_torch()
+    dev = _torch.cuda.current_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"expected tensors on the current device cuda:{dev}, got {t.device}")
+    return dev
 
 
-def _want(t, what, shape, *dtypes):
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}"
+def _stream_on(dev, stream):
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _want(t, what, shape, dtype=None):
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor of shape {shape}, got {tuple(t.shape)}"
                          f"{'' if t.is_contiguous() else ', not contiguous'}")
-    if dtypes and str(t.dtype) not in dtypes:
-        raise ValueError(f"{what}: expected {' or '.join(dtypes)}, got {t.dtype}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
 
 
 def _rows_of(t, what):
     """(rows, cols, stride) of a matrix whose rows are contiguous."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: expected a 2-d tensor with contiguous rows")
+    if t.dim() != 2:
+        raise ValueError(f"{what}: expected a 2-d tensor")
     rows, cols = t.shape
-    return rows, cols, t.stride(0) if rows > 1 else cols
-
-
-_I32, _F32, _U8 = ("torch.int32",), ("torch.float32",), ("torch.uint8",)
+    stride, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{what}: expected contiguous rows")
+    return rows, cols, stride if rows > 1 else cols
 
 
 def make_router(*, score=MOE_SCORE_SOFTMAX, num_groups=1, top_groups=1, group_score=MOE_GROUP_MAX,
@@ -464,7 +485,8 @@ def make_router(*, score=MOE_SCORE_SOFTMAX, num_groups=1, top_groups=1, group_sc
     r.score, r.num_groups, r.top_groups, r.group_score = score, num_groups, top_groups, group_score
     r.renormalize, r.scale = int(renormalize), scale
     if bias is not None:
-        _want(bias, "bias", (bias.numel(),), *_F32)
+        _on_current_device(bias)
+        _want(bias, "bias", (bias.numel(),), _F32)
     r.bias_dev = _dev_ptr(bias)
     r._keep = bias
     return r
@@ -482,12 +504,12 @@ def moe_route(router: moe_router_t, logits, K: int, ids, w, stream=None) -> None
     """logits [T, E] float32 or bfloat16, rows may be strided; ids int32 and
     w float32 [T, K] receive the routes."""
     T, E, stride = _rows_of(logits, "logits")
-    _on_current_device(logits, ids, w)
+    dev = _on_current_device(logits, ids, w)
     _check_bias(router, E)
-    _want(ids, "ids", (T, K), *_I32)
-    _want(w, "w", (T, K), *_F32)
+    _want(ids, "ids", (T, K), _I32)
+    _want(w, "w", (T, K), _F32)
     _check(lib().moe_route(C.byref(router), _type_of(logits, "logits"), logits.data_ptr(), stride, T, E, K,
-                           ids.data_ptr(), w.data_ptr(), _stream(stream)))
+                           ids.data_ptr(), w.data_ptr(), _stream_on(dev, stream)))
 
 
 def moe_layer_decode_router(cache: Cache, layer: int, x, logits, K: int, out, router=None, shared=None,
@@ -505,15 +527,15 @@ def moe_layer_decode_router(cache: Cache, layer: int, x, logits, K: int, out, ro
 def _row_args(fmt, dense, what, codes, scales, globals, rows_per_global):
     rows, cols, stride = _rows_of(dense, what)
     blk = 32 if fmt == MOE_FMT_MXFP4 else 16
-    _on_current_device(dense, codes, scales, globals)
+    dev = _on_current_device(dense, codes, scales, globals)
     if cols % blk == 0:   # other widths are the library's to refuse
-        _want(codes, "codes", (rows, cols // 2), *_U8)
-        _want(scales, "scales", (rows, cols // blk), *_U8)
+        _want(codes, "codes", (rows, cols // 2), _U8)
+        _want(scales, "scales", (rows, cols // blk), _U8)
     if globals is not None:
         if rows_per_global < 1:
             raise ValueError("globals need rows_per_global >= 1")
-        _want(globals, "globals", (-(-rows // rows_per_global),), *_F32)
-    return rows, cols, stride
+        _want(globals, "globals", (-(-rows // rows_per_global),), _F32)
+    return rows, cols, stride, dev
 
 
 def moe_quantize_rows(fmt: int, src, codes, scales, globals=None, rows_per_global: int = 0,
@@ -521,21 +543,21 @@ def moe_quantize_rows(fmt: int, src, codes, scales, globals=None, rows_per_globa
     """src [rows, cols] float32 or bfloat16, rows may be strided -> codes
     uint8 [rows, cols/2], scales uint8 [rows, cols/B]; globals float32
     [ceil(rows / rows_per_global)] (E2M1) or None."""
-    rows, cols, stride = _row_args(fmt, src, "src", codes, scales, globals, rows_per_global)
+    rows, cols, stride, dev = _row_args(fmt, src, "src", codes, scales, globals, rows_per_global)
     _check(lib().moe_quantize_rows(
         fmt, _type_of(src, "src"), src.data_ptr(), stride, rows, cols,
         None if globals is None else globals.data_ptr(), rows_per_global, codes.data_ptr(), scales.data_ptr(),
-        _stream(stream)))
+        _stream_on(dev, stream)))
 
 
 def moe_dequantize_rows(fmt: int, codes, scales, dst, globals=None, rows_per_global: int = 0,
                         stream=None) -> None:
     """The inverse: the values of the rows into dst [rows, cols] (float32 or
     bfloat16, rows may be strided)."""
-    rows, cols, stride = _row_args(fmt, dst, "dst", codes, scales, globals, rows_per_global)
+    rows, cols, stride, dev = _row_args(fmt, dst, "dst", codes, scales, globals, rows_per_global)
     _check(lib().moe_dequantize_rows(
         fmt, codes.data_ptr(), scales.data_ptr(), rows, cols, None if globals is None else globals.data_ptr(),
-        rows_per_global, _type_of(dst, "dst"), dst.data_ptr(), stride, _stream(stream)))
+        rows_per_global, _type_of(dst, "dst"), dst.data_ptr(), stride, _stream_on(dev, stream)))
 
 
 def make_mx_bank(codes, scales) -> moe_mx_bank_t:
@@ -544,8 +566,9 @@ def make_mx_bank(codes, scales) -> moe_mx_bank_t:
     if codes.dim() != 3:
         raise ValueError("codes: expected [num_rows, n, k/2]")
     P, n, half = codes.shape
-    _want(codes, "codes", (P, n, half), *_U8)
-    _want(scales, "scales", (P, n, half // 16), *_U8)
+    _on_current_device(codes, scales)
+    _want(codes, "codes", (P, n, half), _U8)
+    _want(scales, "scales", (P, n, half // 16), _U8)
     b = moe_mx_bank_t()
     b.num_rows, b.n, b.k = P, n, 2 * half
     b.codes_dev, b.scales_dev = _dev_ptr(codes), _dev_ptr(scales)
@@ -561,21 +584,21 @@ def moe_mx_product(bank: moe_mx_bank_t, x, idx, out, workspace, swiglu: bool = F
     """x [T, k] bfloat16 (rows may be strided), idx int32 [T, K] or None,
     out [T * K, n or n/2] float32 or bfloat16."""
     T, k, stride = _rows_of(x, "x")
-    _on_current_device(x, idx, out, workspace, *getattr(bank, "_keep", ()))
+    dev = _on_current_device(x, idx, out, workspace, *bank._keep)
     if k != bank.k:
         raise ValueError(f"x has {k} columns, the bank's matrices {bank.k}")
     if _type_of(x, "x") != MOE_TYPE_BF16:
         raise ValueError("x must be bfloat16")
     K = 1 if idx is None else idx.shape[-1]
     if idx is not None:
-        _want(idx, "idx", (T, K), *_I32)
+        _want(idx, "idx", (T, K), _I32)
     _want(out, "out", (T * K, bank.n // 2 if swiglu else bank.n))
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     _check(lib().moe_mx_product(
         C.byref(bank), x.data_ptr(), stride, None if idx is None else idx.data_ptr(), T, K, int(swiglu),
         _type_of(out, "out"), out.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        workspace.nbytes, _stream_on(dev, stream)))
 
 
 def moe_routed_mx_workspace_bytes(num_rows: int, hidden: int, ffn: int, T: int, K: int) -> int:
@@ -585,18 +608,18 @@ def moe_routed_mx_workspace_bytes(num_rows: int, hidden: int, ffn: int, T: int, 
 def moe_routed_decode_mx(pool: moe_pool_t, x, idx, w, out, workspace, addend=None, stream=None) -> None:
     """moe_routed_decode with MXFP4 activations over an MXFP4 pool."""
     T, K = idx.shape
-    _on_current_device(x, idx, w, out, workspace, addend)
+    dev = _on_current_device(x, idx, w, out, workspace, addend)
     if _type_of(x, "x") != MOE_TYPE_BF16 or _type_of(out, "out") != MOE_TYPE_BF16:
         raise ValueError("x and out must be bfloat16")
     _want(x, "x", (T, pool.hidden))
-    _want(idx, "idx", (T, K), *_I32)
-    _want(w, "w", (T, K), *_F32)
+    _want(idx, "idx", (T, K), _I32)
+    _want(w, "w", (T, K), _F32)
     _want(out, "out", (T, pool.hidden))
     if addend is not None:
-        _want(addend, "addend", (T, pool.hidden), *_F32)
+        _want(addend, "addend", (T, pool.hidden), _F32)
     _check(lib().moe_routed_decode_mx(
         C.byref(pool), _dev_ptr(x), _dev_ptr(idx), _dev_ptr(w), T, K, _dev_ptr(addend), _dev_ptr(out),
-        _dev_ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+        _dev_ptr(workspace), workspace.nbytes, _stream_on(dev, stream)))
 
 
 # ---------------------------------------------------------------- inspection

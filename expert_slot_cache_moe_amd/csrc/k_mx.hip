@@ -40,9 +40,6 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb
 
 __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
 
-__device__ __forceinline__ void store_out(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store_out(uint16_t *p, float v) { *p = f32_to_bf16(v); }
-
 // Four consecutive outputs col .. col + 3 of a row of cols; `whole`: rows
 // start on whole vectors of four and cols is a multiple of 4.
 __device__ __forceinline__ void store4(float *o, int col, int cols, bool whole, f32x4 v) {
@@ -77,7 +74,7 @@ struct MxWs {
     size_t n_runs, runs, routes, codes, scales, total;
     int64_t max_runs;
 };
-constexpr int kRunLength = kTile;
+constexpr int kRunLength = kTile;   // the shortest run
 
 MxWs mx_ws(int P, int k, int T, int K) {
     auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
@@ -164,69 +161,468 @@ __global__ __launch_bounds__(kGroupThreads) void mx_group_kernel(const int32_t *
 
 constexpr int kWaves = 4, kThreads = kWaves * kWave;
 
-// One block: 16 output columns (with SwiGLU 16 gate and 16 up rows of the
-// matrix) for one run of up to 16 routes; the waves take every fourth step
-// of k and add their sums in LDS, in wave order.
-template <bool SWIGLU, typename OUT>
-__global__ __launch_bounds__(kThreads) void mx_stream_kernel(MxParams p, const uint8_t *__restrict__ xc,
-                                                             const uint8_t *__restrict__ xs,
-                                                             const int32_t *__restrict__ n_runs,
-                                                             const Run *__restrict__ runs,
-                                                             const int32_t *__restrict__ routes, int R,
-                                                             OUT *__restrict__ out) {
-    constexpr int kM = SWIGLU ? 2 : 1;
-    __shared__ f32x4 part[kWaves][kM][kWave];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int c = lane & (kTile - 1), q = lane / kTile;
-    Run run;
-    if (n_runs != nullptr) {
-        if ((int)blockIdx.y >= n_runs[0]) return;
-        run = runs[blockIdx.y];
-    } else {
-        run = Run{0, (int)blockIdx.y * kRunLength, min(kRunLength, R - (int)blockIdx.y * kRunLength), 0};
+// Short runs: 16 NT routes of one matrix row at a time against columns of
+// 16, the matrix straight from memory to registers (it is read once, so
+// nothing is gained by passing it through LDS), x quantised where it is
+// needed, so that no launch of its own has to do that first.
+//
+// Lists of routes come in three ways:
+//   kRuns    from mx_group_kernel (or, without ids, consecutive rows);
+//   kByRoute slot r is route r: the first route of its matrix row takes all
+//            of that row's routes, the others leave;
+//   kByRow   slot i is matrix row i, slot P the routes without a row.
+// The last two look through idx in the block itself: few routes, no launch
+// for the lists.
+enum ListMode : int { kRuns, kByRoute, kByRow };
+constexpr int kInlineRoutes = 2048, kIdxPerThread = kInlineRoutes / kThreads;
+static_assert(kIdxPerThread * kWaves <= kWave, "one lane for each count");
+
+// A barrier that orders LDS alone: loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+struct ListLds {
+    int32_t routes[kInlineRoutes];
+    int32_t counts[kIdxPerThread * kWaves];
+};
+
+struct RouteList {
+    int row = -1, count = 0, start = 0;
+    const int32_t *at = nullptr;             // in LDS or memory; NULL: start, start + 1, ...
+    __device__ __forceinline__ int route(int i) const { return at != nullptr ? at[i] : start + i; }
+};
+
+// The ids of idx that one of 256 threads looks through.
+struct IdxPart {
+    int32_t r[kIdxPerThread];
+    // (no load here is conditional, so the compiler can count what is in flight)
+    __device__ __forceinline__ void load(const int32_t *idx, int tid, int R) {
+#pragma unroll
+        for (int k = 0; k < kIdxPerThread; ++k) r[k] = idx[min(k * kThreads + tid, R - 1)];
     }
-    const int cols = SWIGLU ? p.n / 2 : p.n;
-    const int j0 = blockIdx.x * kTile;
-    const int at = run.start + min(c, run.count - 1);
-    const int route = n_runs != nullptr ? routes[at] : at;
-    f32x4 acc[kM];
+};
+
+// The matrix row of an inline list's slot; -1: routes without a row.
+__device__ __forceinline__ int slot_row(const MxParams &p, int mode, int slot) {
+    const int row = mode == kByRoute ? p.idx[slot] : slot;
+    return __builtin_amdgcn_readfirstlane(row < 0 || row >= p.P ? -1 : row);
+}
+
+// Collects the routes of `row`, ascending, into the block's list and returns
+// their number.  (Blocks that share a list must agree on its order.)
+__device__ __forceinline__ int collect(const IdxPart &part, ListLds &lds, const MxParams &p, int row, int R) {
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    uint64_t m[kIdxPerThread];
 #pragma unroll
-    for (int m = 0; m < kM; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (run.row >= 0) {
-        const int nblk = p.k / 32, steps = (p.k + kStep - 1) / kStep;
-        const int64_t token = route / p.K;
-        const uint8_t *bx = xc + token * (p.k / 2), *bs = xs + token * nblk;
-        const uint8_t *ax[kM], *as[kM];
+    for (int k = 0; k < kIdxPerThread; ++k) {
+        const int v = part.r[k] < 0 || part.r[k] >= p.P ? -1 : part.r[k];
+        m[k] = __ballot(k * kThreads + tid < R && v == row);
+        if (lane == 0) lds.counts[k * kWaves + wave] = __popcll(m[k]);
+    }
+    lds_barrier();
+    const int n = lane < kIdxPerThread * kWaves ? lds.counts[lane] : 0;
+    const int incl = wave_inclusive_sum(n);
 #pragma unroll
-        for (int m = 0; m < kM; ++m) {
-            const int64_t r = (int64_t)run.row * p.n + m * cols + min(j0 + c, cols - 1);
-            ax[m] = p.codes + r * (p.k / 2);
-            as[m] = p.scales + r * nblk;
-        }
-        for (int s = wave; s < steps; s += kWaves) {
-            const int b = 4 * s + q, bc = min(b, nblk - 1);
-            const u32x4 bv = reinterpret_cast<const u32x4 *>(bx)[bc];
-            const uint32_t sb = b < nblk ? bs[bc] : 0u;
+    for (int k = 0; k < kIdxPerThread; ++k) {
+        if (m[k] == 0) continue;
+        const int base = __builtin_amdgcn_readlane(incl - n, k * kWaves + wave);
+        if ((m[k] >> lane) & 1)
+            lds.routes[base + __builtin_amdgcn_mbcnt_hi((uint32_t)(m[k] >> 32),
+                                                        __builtin_amdgcn_mbcnt_lo((uint32_t)m[k], 0u))] =
+                k * kThreads + tid;
+    }
+    lds_barrier();
+    return __builtin_amdgcn_readlane(incl, kWave - 1);
+}
+
+// The list of slot `slot` of a launch without inline lists; false: none.
+__device__ __forceinline__ bool run_list(RouteList &l, int slot, int run_length, const int32_t *n_runs,
+                                         const Run *runs, const int32_t *routes, int R) {
+    if (n_runs != nullptr) {
+        if (slot >= n_runs[0]) return false;
+        const Run run = runs[slot];
+        l.row = run.row;
+        l.count = run.count;
+        l.at = routes + run.start;
+    } else {
+        l.row = 0;
+        l.start = slot * run_length;
+        l.count = min(run_length, R - l.start);
+    }
+    return true;
+}
+
+// Zeros in columns [j0, j0 + width) of every route of a list, by THREADS threads.
+template <int THREADS>
+__device__ __forceinline__ void zero_rows(const MxParams &p, const RouteList &l, int cols, int j0, int width, int tid) {
+    width = min(width, cols - j0);
+    if (width <= 0) return;
+    for (int i = tid; i < l.count * width; i += THREADS) {
+        const int t = i / width;
+        const int64_t o = (int64_t)l.route(t) * cols + j0 + (i - t * width);
+        if (p.out_type == MOE_TYPE_F32)
+            static_cast<float *>(p.out)[o] = 0.f;
+        else
+            static_cast<uint16_t *>(p.out)[o] = 0;
+    }
+}
+
+// Four columns of a route's result: the sums, or silu(gate) * up of them.
+template <bool SWIGLU, int kM>
+__device__ __forceinline__ void store_columns(const MxParams &p, bool f32_out, int route, int cols, int col,
+                                              bool whole, f32x4 (&v)[kM]) {
+    if constexpr (SWIGLU) {
 #pragma unroll
-            for (int m = 0; m < kM; ++m) {
-                const u32x4 av = reinterpret_cast<const u32x4 *>(ax[m])[bc];
-                const uint32_t sa = b < nblk ? as[m][bc] : 0u;
-                acc[m] = mfma(av, sa, bv, sb, acc[m]);
+        for (int i = 0; i < 4; ++i) v[0][i] = silu(v[0][i]) * v[kM - 1][i];
+    }
+    if (f32_out)
+        store4(static_cast<float *>(p.out) + (int64_t)route * cols, col, cols, whole, v[0]);
+    else
+        store4(static_cast<uint16_t *>(p.out) + (int64_t)route * cols, col, cols, whole, v[0]);
+}
+
+// The scale bytes of a row for U steps: lane quarter q uses byte q of each
+// step's four.  VEC: whole, aligned vectors (k a multiple of 128 U).
+template <int U, bool VEC> struct StepScales {
+    uint32_t v[U];
+    __device__ __forceinline__ void load(const uint8_t *row, int s0, int nblk, int q) {
+        if constexpr (VEC && U == 4) {
+            const u32x4 t = *reinterpret_cast<const u32x4 *>(row + 4 * s0);
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = t[u];
+        } else if constexpr (VEC && U == 2) {
+            const uint2 t = *reinterpret_cast<const uint2 *>(row + 4 * s0);
+            v[0] = t.x;
+            v[1] = t.y;
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int b = 4 * (s0 + u) + q;
+                const uint32_t t = row[min(b, nblk - 1)];
+                v[u] = b < nblk ? t : 0u;
             }
         }
     }
-#pragma unroll
-    for (int m = 0; m < kM; ++m) part[wave][m][lane] = acc[m];
-    __syncthreads();
-    if (wave != 0) return;
-#pragma unroll
-    for (int m = 0; m < kM; ++m)
-        for (int v = 1; v < kWaves; ++v) acc[m] += part[v][m][lane];
-    if (c >= run.count) return;
-    OUT *o = out + (int64_t)route * cols + j0 + 4 * q;
+    __device__ __forceinline__ uint32_t at(int u, int q) const { return VEC ? v[u] >> (8 * q) : v[u]; }
+};
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+// 32 bf16 as an MX block: codes and scale byte (0xFF and zeros where one of
+// them is NaN or infinite).  x / scale is exact, so the scaled conversion's
+// one rounding is the format's.
+__device__ __forceinline__ u32x4 quantize_block(const u32x4 (&x)[4], uint32_t &scale) {
+    u16x2 m = {0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (j0 + 4 * q + i < cols) store_out(o + i, SWIGLU ? silu(acc[0][i]) * acc[kM - 1][i] : acc[0][i]);
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, x[i][d] & 0x7fff7fffu));
+    const int a = max((int)m[0], (int)m[1]);
+    const bool bad = a >= 0x7f80;
+    const int e = max((a >> 7) - 2, 0);
+    const float f = __uint_as_float((uint32_t)e << 23);
+    u32x4 c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t t = 0;
+        // (a bit cast of a vector's element itself would take its first one)
+#define MOE_CVT(B)                                                                                    \
+    {                                                                                                 \
+        const uint32_t pair = x[i][B];                                                                \
+        t = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(t, __builtin_bit_cast(bf16x2, pair), f, B);     \
+    }
+        MOE_CVT(0)
+        MOE_CVT(1)
+        MOE_CVT(2)
+        MOE_CVT(3)
+#undef MOE_CVT
+        c[i] = bad ? 0u : t;
+    }
+    scale = bad ? 0xFFu : (uint32_t)e;
+    return c;
+}
+
+// A 64-byte block of a row of x, as 32 bf16.
+__device__ __forceinline__ void load_block(const uint16_t *x, bool vec, u32x4 (&v)[4]) {
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const u32x4 *>(x)[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) v[i][d] = x[8 * i + 2 * d] | ((uint32_t)x[8 * i + 2 * d + 1] << 16);
+    }
+}
+
+// A lane's codes and scales of U steps of kM matrix rows.
+template <int U, bool VEC, int kM> struct MatrixChunk {
+    u32x4 a[kM][U];
+    StepScales<U, VEC> s[kM];
+    __device__ __forceinline__ void load(const uint8_t *const (&ax)[kM], const uint8_t *const (&as)[kM], int s0,
+                                         int nblk, int q) {
+#pragma unroll
+        for (int m = 0; m < kM; ++m) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int b = 4 * (s0 + u) + q;
+                a[m][u] = reinterpret_cast<const u32x4 *>(ax[m])[VEC ? b : min(b, nblk - 1)];
+            }
+            s[m].load(as[m], s0, nblk, q);
+        }
+    }
+};
+
+// Few blocks: the four waves of a block share 16 output columns (with
+// SwiGLU 16 gate and 16 up rows) and split k, every fourth chunk of U steps
+// each; their sums are added in LDS, in wave order.  A lane's part of x for
+// one step is one whole MX block of one token, quantised in registers.
+template <bool SWIGLU, int U, bool VEC, int NT, bool INLINE>
+__global__ __launch_bounds__(kThreads) void mx_split_kernel(MxParams p, int mode, bool x_vec,
+                                                            const int32_t *__restrict__ n_runs,
+                                                            const Run *__restrict__ runs,
+                                                            const int32_t *__restrict__ routes, int R) {
+    constexpr int kM = SWIGLU ? 2 : 1;
+    __shared__ f32x4 part[kWaves][kM][NT][kWave];
+    __shared__ ListLds lds;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    const int c = lane & (kTile - 1), q = lane / kTile;
+    const int cols = SWIGLU ? p.n / 2 : p.n;
+    const int j0 = blockIdx.x * kTile;
+    const int nblk = p.k / 32, steps = (p.k + kStep - 1) / kStep;
+    const int last = (steps - 1) / U * U;    // the last chunk; requests past it repeat it
+
+    MatrixChunk<U, VEC, kM> w;
+    const uint8_t *ax[kM], *as[kM];
+    RouteList l;
+    auto request = [&](int row) {
+#pragma unroll
+        for (int m = 0; m < kM; ++m) {
+            const int64_t r = (int64_t)max(row, 0) * p.n + m * cols + min(j0 + c, cols - 1);
+            ax[m] = p.codes + r * nblk * 16;
+            as[m] = p.scales + r * nblk;
+        }
+        w.load(ax, as, min(wave * U, last), nblk, q);
+    };
+    if constexpr (INLINE) {
+        // the matrix is requested right behind the ids, before they are looked through
+        IdxPart part;
+        part.load(p.idx, tid, R);
+        l.row = slot_row(p, mode, blockIdx.y);
+        request(l.row);
+        l.count = collect(part, lds, p, l.row, R);
+        l.at = lds.routes;
+        if (l.count == 0 || (mode == kByRoute && lds.routes[0] < (int)blockIdx.y)) return;
+    } else {
+        if (!run_list(l, blockIdx.y, kTile * NT, n_runs, runs, routes, R)) return;
+        request(l.row);
+    }
+    if (l.row < 0) {
+        zero_rows<kThreads>(p, l, cols, j0, kTile, tid);
+        return;
+    }
+    const bool f32_out = p.out_type == MOE_TYPE_F32;
+    const bool whole = cols % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & (f32_out ? 15 : 7)) == 0;
+
+    for (int base = 0; base < l.count; base += kTile * NT) {
+        f32x4 acc[kM][NT];
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        int route[NT];
+        const uint16_t *xr[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            route[t] = l.route(min(base + t * kTile + c, l.count - 1));
+            xr[t] = p.x + (int64_t)(route[t] / p.K) * p.x_stride;
+        }
+        {
+            for (int s0 = wave * U; s0 < steps; s0 += kWaves * U) {
+                // the first pass's first chunk is there already
+                if (base > 0 || s0 != wave * U) w.load(ax, as, s0, nblk, q);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (t > 0 && base + t * kTile >= l.count) break;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int b = 4 * (s0 + u) + q;
+                        u32x4 xv[4];
+                        load_block(xr[t] + 32 * (VEC ? b : min(b, nblk - 1)), x_vec, xv);
+                        uint32_t sb;
+                        const u32x4 bv = quantize_block(xv, sb);
+                        if (!VEC && b >= nblk) sb = 0u;
+#pragma unroll
+                        for (int m = 0; m < kM; ++m) acc[m][t] = mfma(w.a[m][u], w.s[m].at(u, q), bv, sb, acc[m][t]);
+                    }
+                }
+            }
+        }
+        if (base > 0) lds_barrier();         // the last pass has read its sums
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) part[wave][m][t][lane] = acc[m][t];
+        lds_barrier();
+        // wave t adds and stores the pass's tile t
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (wave != t || base + t * kTile + c >= l.count) continue;
+            f32x4 v[kM];
+#pragma unroll
+            for (int m = 0; m < kM; ++m) {
+                v[m] = part[0][m][t][lane];
+#pragma unroll
+                for (int o = 1; o < kWaves; ++o) v[m] += part[o][m][t][lane];
+            }
+            store_columns<SWIGLU>(p, f32_out, route[t], cols, j0 + 4 * q, whole, v);
+        }
+    }
+}
+
+// Many blocks: each of the four waves has 16 output columns (with SwiGLU 16
+// gate and 16 up rows; without, 32 columns) of its own over all of k, and
+// the block quantises its routes' x into LDS once for all four, 64 MX
+// blocks of k at a time.  LDS holds codes by (block of k, token), 16 bytes
+// each, so that an operand read is 1 KB in a row.
+//
+// A wave's loads return in order.  So the first part of x is requested
+// first and the matrix behind it: x is quantised while the matrix, two
+// chunks of U steps at once, is on its way.  Where those are all of k they
+// serve every pass over a long list.
+constexpr int kSpanBlocks = 64;
+
+template <bool SWIGLU, int U, bool VEC, bool INLINE>
+__global__ __launch_bounds__(kThreads, 3) void mx_stream_kernel(MxParams p, int mode, bool x_vec, int slots,
+                                                             int pass_blocks, const int32_t *__restrict__ n_runs,
+                                                             const Run *__restrict__ runs,
+                                                             const int32_t *__restrict__ routes, int R) {
+    constexpr int kM = 2;
+    constexpr int kCols = SWIGLU ? kTile : 2 * kTile;       // output columns of a wave
+    __shared__ __align__(16) u32x4 xc[kSpanBlocks][kTile];
+    __shared__ uint8_t xs[kSpanBlocks][kTile];
+    __shared__ ListLds lds;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    const int c = lane & (kTile - 1), q = lane / kTile;
+    // Lists vary fastest: workgroups go to the eight XCDs in turn, and blocks
+    // with work and blocks without (no such list, no such pass) must not fall
+    // to different ones.
+    const int slot = blockIdx.x % slots, rest = blockIdx.x / slots;
+    const int pass = rest % pass_blocks, cb = rest / pass_blocks;
+    const int cols = SWIGLU ? p.n / 2 : p.n;
+    const int j0 = (cb * kWaves + wave) * kCols;
+    const int nblk = p.k / 32, steps = (p.k + kStep - 1) / kStep;
+    const int last = (steps - 1) / U * U;    // the last chunk; requests past it repeat it
+
+    RouteList l;
+    if constexpr (INLINE) {
+        IdxPart part;
+        part.load(p.idx, tid, R);
+        l.row = slot_row(p, mode, slot);
+        l.count = collect(part, lds, p, l.row, R);
+        l.at = lds.routes;
+        if (l.count <= pass * kTile || (mode == kByRoute && lds.routes[0] < slot)) return;
+    } else if (!run_list(l, slot, kTile, n_runs, runs, routes, R)) {
+        return;
+    }
+    if (l.row < 0) {
+        if (pass == 0) zero_rows<kThreads>(p, l, cols, cb * kWaves * kCols, kWaves * kCols, tid);
+        return;
+    }
+
+    // x: lanes over blocks of one token, or of two or four where k is short
+    const int shift = nblk > 32 ? 6 : nblk > 16 ? 5 : 4;
+    const int xb = tid & ((1 << shift) - 1), xt = tid >> shift, per = kThreads >> shift;
+    u32x4 xv[4];
+    auto x_load = [&](int base, int b0, int t) {     // rows past the list and blocks past the row repeat the last
+        const int64_t token = l.route(min(base + t, l.count - 1)) / p.K;
+        load_block(p.x + token * p.x_stride + 32 * min(b0 + xb, nblk - 1), x_vec, xv);
+    };
+    auto x_put = [&](int t) {
+        uint32_t sb;
+        const u32x4 codes = quantize_block(xv, sb);
+        xc[xb][t] = codes;
+        xs[xb][t] = (uint8_t)sb;
+    };
+    x_load(pass * kTile, 0, xt);
+
+    MatrixChunk<U, VEC, kM> w[2];
+    const uint8_t *ax[kM], *as[kM];
+#pragma unroll
+    for (int m = 0; m < kM; ++m) {
+        const int j = SWIGLU ? min(j0 + c, cols - 1) + m * cols : min(j0 + m * kTile + c, cols - 1);
+        const int64_t r = (int64_t)l.row * p.n + j;
+        ax[m] = p.codes + r * nblk * 16;
+        as[m] = p.scales + r * nblk;
+    }
+    w[0].load(ax, as, 0, nblk, q);
+    w[1].load(ax, as, min(U, last), nblk, q);
+    const bool f32_out = p.out_type == MOE_TYPE_F32;
+    const bool whole = cols % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & (f32_out ? 15 : 7)) == 0;
+
+    bool again = false;
+    for (int base = pass * kTile; base < l.count; base += pass_blocks * kTile) {
+        f32x4 acc[kM];
+#pragma unroll
+        for (int m = 0; m < kM; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const int live = min(l.count - base, kTile);
+        if (again && steps > 2 * U) {
+            w[0].load(ax, as, 0, nblk, q);
+            w[1].load(ax, as, min(U, last), nblk, q);
+        }
+        for (int b0 = 0; b0 < nblk; b0 += kSpanBlocks) {
+            const int nb = min(kSpanBlocks, nblk - b0);
+            if (again) {
+                lds_barrier();               // the span before has been read
+                x_load(base, b0, xt);
+            }
+            again = true;
+            x_put(xt);
+            for (int t = xt + per; t < live; t += per) {
+                x_load(base, b0, t);
+                x_put(t);
+            }
+            lds_barrier();
+            const int s_end = (min(b0 + kSpanBlocks, nblk) + 3) / 4;
+            auto chunk = [&](int s0, const MatrixChunk<U, VEC, kM> &m0) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int b = 4 * (s0 + u) + q - b0, bc = VEC ? b : min(b, nb - 1);
+                    const int tc = min(c, live - 1);
+                    const u32x4 bv = xc[bc][tc];
+                    const uint32_t sb = VEC || b < nb ? xs[bc][tc] : 0u;
+#pragma unroll
+                    for (int m = 0; m < kM; ++m) acc[m] = mfma(m0.a[m][u], m0.s[m].at(u, q), bv, sb, acc[m]);
+                }
+            };
+            for (int s0 = b0 / 4; s0 < s_end; s0 += 2 * U) {
+                chunk(s0, w[0]);
+                if (steps > 2 * U) w[0].load(ax, as, min(s0 + 2 * U, last), nblk, q);
+                if (s0 + U < s_end) {
+                    chunk(s0 + U, w[1]);
+                    if (steps > 2 * U) w[1].load(ax, as, min(s0 + 3 * U, last), nblk, q);
+                }
+            }
+        }
+        if (c < live) {
+            const int route = l.route(base + c);
+            if constexpr (SWIGLU) {
+                f32x4 v[kM] = {acc[0], acc[1]};
+                store_columns<true>(p, f32_out, route, cols, j0 + 4 * q, whole, v);
+            } else {
+#pragma unroll
+                for (int m = 0; m < kM; ++m) {
+                    f32x4 v[1] = {acc[m]};
+                    store_columns<false>(p, f32_out, route, cols, j0 + m * kTile + 4 * q, whole, v);
+                }
+            }
+        }
+    }
 }
 
 // Long runs: a block takes 256 rows of the matrix (with SwiGLU 128 gate and
@@ -438,18 +834,55 @@ size_t mx_workspace_bytes(int P, int n, int k, int T, int K) {
 
 namespace {
 
-template <typename OUT>
-hipError_t launch_stream(const MxParams &p, const uint8_t *xc, const uint8_t *xs, const int32_t *n_runs,
-                         const Run *runs, const int32_t *routes, int R, int64_t max_runs, hipStream_t s) {
+// Blocks of the many-block form that keep the device busy; with fewer, k is
+// split over the waves instead.
+constexpr int64_t kManyBlocks = 512;
+// Blocks for the passes over one matrix row's list, where lists may be long.
+constexpr int kPassBlocks = 2;
+
+template <bool SWIGLU, bool INLINE>
+hipError_t launch_stream_shape(const MxParams &p, int mode, const int32_t *n_runs, const Run *runs,
+                               const int32_t *routes, int R, int64_t slots, hipStream_t s) {
     const int cols = p.swiglu ? p.n / 2 : p.n;
-    const dim3 grid((cols + kTile - 1) / kTile, (unsigned)max_runs);
-    if (p.swiglu)
-        hipLaunchKernelGGL((mx_stream_kernel<true, OUT>), grid, dim3(kThreads), 0, s, p, xc, xs, n_runs, runs,
-                           routes, R, static_cast<OUT *>(p.out));
-    else
-        hipLaunchKernelGGL((mx_stream_kernel<false, OUT>), grid, dim3(kThreads), 0, s, p, xc, xs, n_runs, runs,
-                           routes, R, static_cast<OUT *>(p.out));
+    const bool x_vec = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.x_stride % 8 == 0;
+    const uintptr_t sp = reinterpret_cast<uintptr_t>(p.scales);
+    const int block_cols = kWaves * (SWIGLU ? 1 : 2) * kTile;
+    const int wide = (cols + block_cols - 1) / block_cols, passes = mode == kByRow ? kPassBlocks : 1;
+    if (wide * slots >= kManyBlocks) {
+        const dim3 grid((unsigned)(wide * slots * passes));
+#define MOE_STREAM(U, VEC)                                                                                     \
+    hipLaunchKernelGGL((mx_stream_kernel<SWIGLU, U, VEC, INLINE>), grid, dim3(kThreads), 0, s, p, mode, x_vec, \
+                       (int)slots, passes, n_runs, runs, routes, R)
+        if (p.k % 512 == 0 && sp % 16 == 0)
+            MOE_STREAM(2, true);
+        else if (p.k % 256 == 0 && sp % 8 == 0)
+            MOE_STREAM(2, true);
+        else
+            MOE_STREAM(2, false);
+#undef MOE_STREAM
+    } else {
+        const dim3 grid((cols + kTile - 1) / kTile, (unsigned)slots);
+#define MOE_SPLIT(U, VEC)                                                                                       \
+    hipLaunchKernelGGL((mx_split_kernel<SWIGLU, U, VEC, 1, INLINE>), grid, dim3(kThreads), 0, s, p, mode, x_vec, \
+                       n_runs, runs, routes, R)
+        if (p.k % 512 == 0 && p.k >= 2048 && sp % 16 == 0)
+            MOE_SPLIT(4, true);
+        else if (p.k % 256 == 0 && sp % 8 == 0)
+            MOE_SPLIT(2, true);
+        else
+            MOE_SPLIT(2, false);
+#undef MOE_SPLIT
+    }
     return hipGetLastError();
+}
+
+hipError_t launch_stream(const MxParams &p, int mode, const int32_t *n_runs, const Run *runs,
+                         const int32_t *routes, int R, int64_t slots, hipStream_t s) {
+    if (mode == kRuns)
+        return p.swiglu ? launch_stream_shape<true, false>(p, mode, n_runs, runs, routes, R, slots, s)
+                        : launch_stream_shape<false, false>(p, mode, n_runs, runs, routes, R, slots, s);
+    return p.swiglu ? launch_stream_shape<true, true>(p, mode, n_runs, runs, routes, R, slots, s)
+                    : launch_stream_shape<false, true>(p, mode, n_runs, runs, routes, R, slots, s);
 }
 
 template <int BT, typename OUT>
@@ -478,19 +911,16 @@ hipError_t launch_tile(const MxParams &p, const uint8_t *xc, const uint8_t *xs, 
 // tile that those fill.
 int run_length_for(int R, int P, bool lists) {
     const int mean = lists ? R / std::min(R, P) : R;
-    return mean >= 160 ? 256 : mean >= 64 ? 128 : mean >= 24 ? 64 : kRunLength;
+    return mean >= 160 ? 256 : mean >= 64 ? 128 : mean >= 24 ? 64 : kTile;
 }
 
 template <typename OUT>
-hipError_t launch_typed(const MxParams &p, const uint8_t *xc, const uint8_t *xs, const int32_t *n_runs,
-                        const Run *runs, const int32_t *routes, int R, int run_length, int64_t max_runs,
-                        hipStream_t s) {
-    switch (run_length) {
-    case 256: return launch_tile<256, OUT>(p, xc, xs, n_runs, runs, routes, R, max_runs, s);
-    case 128: return launch_tile<128, OUT>(p, xc, xs, n_runs, runs, routes, R, max_runs, s);
-    case 64: return launch_tile<64, OUT>(p, xc, xs, n_runs, runs, routes, R, max_runs, s);
-    default: return launch_stream<OUT>(p, xc, xs, n_runs, runs, routes, R, max_runs, s);
-    }
+hipError_t launch_tile_for(int run_length, const MxParams &p, const uint8_t *xc, const uint8_t *xs,
+                           const int32_t *n_runs, const Run *runs, const int32_t *routes, int R,
+                           int64_t max_runs, hipStream_t s) {
+    if (run_length == 256) return launch_tile<256, OUT>(p, xc, xs, n_runs, runs, routes, R, max_runs, s);
+    if (run_length == 128) return launch_tile<128, OUT>(p, xc, xs, n_runs, runs, routes, R, max_runs, s);
+    return launch_tile<64, OUT>(p, xc, xs, n_runs, runs, routes, R, max_runs, s);
 }
 
 }  // namespace
@@ -503,13 +933,14 @@ hipError_t launch_mx_product(const MxParams &p, bool reuse_lists, hipStream_t s)
     Run *runs = reinterpret_cast<Run *>(p.ws + L.runs);
     int32_t *routes = reinterpret_cast<int32_t *>(p.ws + L.routes);
     uint8_t *xc = p.ws + L.codes, *xs = p.ws + L.scales;
-    RowsParams rp{};
-    rp.rows = p.T;
-    rp.cols = p.k;
-    rp.stride = p.x_stride;
-    hipError_t e = launch_quantize(MOE_FMT_MXFP4, MOE_TYPE_BF16, rp, p.x, xc, xs, s);
-    if (e != hipSuccess) return e;
     const int run_length = run_length_for(R, p.P, p.idx != nullptr);
+    const bool stream = run_length == kTile;
+    if (p.idx != nullptr && stream && R <= kInlineRoutes) {
+        const bool by_route = R <= p.P;
+        return launch_stream(p, by_route ? kByRoute : kByRow, nullptr, nullptr, nullptr, R,
+                             by_route ? R : p.P + 1, s);
+    }
+    hipError_t e = hipSuccess;
     int64_t max_runs = (R + run_length - 1) / run_length;
     if (p.idx != nullptr) {
         max_runs = std::min<int64_t>(R, (int64_t)p.P + 1) + R / run_length;
@@ -527,9 +958,16 @@ hipError_t launch_mx_product(const MxParams &p, bool reuse_lists, hipStream_t s)
     } else {
         n_runs = nullptr;
     }
+    if (stream) return launch_stream(p, kRuns, n_runs, runs, routes, R, max_runs, s);
+    RowsParams rp{};
+    rp.rows = p.T;
+    rp.cols = p.k;
+    rp.stride = p.x_stride;
+    e = launch_quantize(MOE_FMT_MXFP4, MOE_TYPE_BF16, rp, p.x, xc, xs, s);
+    if (e != hipSuccess) return e;
     return p.out_type == MOE_TYPE_F32
-               ? launch_typed<float>(p, xc, xs, n_runs, runs, routes, R, run_length, max_runs, s)
-               : launch_typed<uint16_t>(p, xc, xs, n_runs, runs, routes, R, run_length, max_runs, s);
+               ? launch_tile_for<float>(run_length, p, xc, xs, n_runs, runs, routes, R, max_runs, s)
+               : launch_tile_for<uint16_t>(run_length, p, xc, xs, n_runs, runs, routes, R, max_runs, s);
 }
 
 }  // namespace moe

@@ -528,7 +528,8 @@ int64_t moe_mx_product_workspace_bytes(int32_t num_rows, int32_t n, int32_t k, i
  * K = 1 (every row takes the one matrix); out_dev: [T K][n or n/2].  A
  * route whose id is outside [0, num_rows) gets a row of zeros.  A NaN scale
  * or a block of x with NaN or infinity makes the outputs that read it NaN.
- * A route's result depends on its row's bytes and its x alone.
+ * Within a call a route's result depends on its row's bytes and its x
+ * alone; calls of other sizes may add in another order.
  * workspace_dev: moe_mx_product_workspace_bytes(...), 256-byte aligned,
  * overwritten; calls that share it must be ordered.  Asynchronous,
  * capturable.  Errors: MOE_INVALID_ARG (sizes, strides, null or misaligned

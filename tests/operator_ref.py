@@ -116,11 +116,13 @@ def product(codes, scales, xq, idx, swiglu=False):
     T, K = idx.shape
     y = np.zeros((T * K, n))
     a = np.zeros((T * K, n))
-    for r, i in enumerate(idx.reshape(-1)):
+    rows = idx.reshape(-1)
+    for i in np.unique(rows):
         if 0 <= i < P:
+            r = np.nonzero(rows == i)[0]
             w = decode_mxfp4(codes[i], scales[i])
-            y[r] = w @ xq[r // K]
-            a[r] = np.abs(w) @ np.abs(xq[r // K])
+            y[r] = xq[r // K] @ w.T
+            a[r] = np.abs(xq[r // K]) @ np.abs(w).T
     if not swiglu:
         return y, a
     g, u = y[:, :n // 2], y[:, n // 2:]

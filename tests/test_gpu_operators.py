@@ -357,6 +357,8 @@ SHAPES = [
     (1, 1, 1, 1, 32), (1, 8, 16, 64, 2048), (1, 3, 5, 15, 64), (2, 2, 3, 17, 96), (3, 1, 2, 16, 128),
     (7, 2, 4, 33, 160), (17, 1, 1, 48, 256), (33, 2, 3, 130, 512), (45, 3, 24, 515, 1056), (5, 4, 40, 260, 4096),
     (64, 8, 6, 128, 384), (130, 2, 3, 80, 1024), (300, 1, 2, 257, 544), (513, 2, 7, 96, 288),
+    (40, 4, 70, 1040, 320), (30, 2, 90, 1101, 2112), (300, 8, 140, 512, 1024), (600, 4, 150, 250, 160),
+    (350, 6, 400, 130, 256), (70, 2, 8, 4100, 480),
 ]
 
 
@@ -371,6 +373,20 @@ def test_product_matches_the_plain_form(T, K, P, n, k, out_dtype):
     _check_product(bank, codes, scales, x, idx, False, out_dtype)
     if n % 2 == 0:
         _check_product(bank, codes, scales, x, idx, True, out_dtype)
+
+
+@pytest.mark.parametrize("T,P,n,k", [(100, 64, 48, 320), (100, 64, 1030, 320), (100, 64, 1030, 2560), (33, 40, 70, 1024),
+                                     (200, 64, 1026, 1024)])
+def test_product_of_one_long_list_among_empty_ones(T, P, n, k):
+    _say("one list", T, P, n, k)
+    g = W.rng(18, "skew", T, P, n, k)
+    bank, codes, scales = _bank(g, P, n, k)
+    x = torch.from_numpy(W.normal_bf16(g, (T, k)).view(np.int16)).cuda().view(torch.bfloat16)
+    idx = np.full((T, 1), P - 3, np.int32)
+    idx[5:9] = -1
+    idx[20] = 0
+    _check_product(bank, codes, scales, x, idx, False, torch.float32)
+    _check_product(bank, codes, scales, x, idx, True, torch.bfloat16)
 
 
 @pytest.mark.parametrize("T,n,k", [(1, 70, 96), (16, 16, 128), (100, 300, 640), (257, 129, 256), (1000, 64, 2048)])
