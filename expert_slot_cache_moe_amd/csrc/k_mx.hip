@@ -105,6 +105,19 @@ MxWs mx_ws(int P, int k, int T, int K) {
 // route's result is independent of its place.
 constexpr int kGroupThreads = 1024, kGroupWaves = kGroupThreads / kWave;
 
+// The next free place of `row`, one for each active lane.  Lanes that share
+// the first lane's row take theirs with one addition (one matrix for all
+// routes is a usual case, and 64 additions to one word take 64 turns).
+__device__ __forceinline__ int place(int32_t *cnt, int row) {
+    const int first = __builtin_amdgcn_readfirstlane(row);
+    const uint64_t same = __ballot(row == first);
+    if (row != first) return atomicAdd(&cnt[row], 1);
+    const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0u));
+    int base = 0;
+    if (before == 0) base = atomicAdd(&cnt[row], __popcll(same));
+    return __builtin_amdgcn_readfirstlane(base) + before;
+}
+
 __global__ __launch_bounds__(kGroupThreads) void mx_group_kernel(const int32_t *__restrict__ idx, int R, int P,
                                                                  int run_length, int32_t *__restrict__ n_runs,
                                                                  Run *__restrict__ runs,
@@ -117,7 +130,8 @@ __global__ __launch_bounds__(kGroupThreads) void mx_group_kernel(const int32_t *
     __syncthreads();
     for (int i = tid; i < R; i += kGroupThreads) {
         const int r = idx[i];
-        atomicAdd(&cnt[r >= 0 && r < P ? r : P], 1);
+        const int row = r >= 0 && r < P ? r : P;
+        place(cnt, row);
     }
     __syncthreads();
     const int per = (P + kGroupThreads) / kGroupThreads;   // rows 0..P
@@ -153,7 +167,8 @@ __global__ __launch_bounds__(kGroupThreads) void mx_group_kernel(const int32_t *
     __syncthreads();
     for (int i = tid; i < R; i += kGroupThreads) {
         const int r = idx[i];
-        routes[atomicAdd(&cnt[r >= 0 && r < P ? r : P], 1)] = i;
+        const int row = r >= 0 && r < P ? r : P;
+        routes[place(cnt, row)] = i;
     }
 }
 
@@ -625,13 +640,18 @@ __global__ __launch_bounds__(kThreads, 3) void mx_stream_kernel(MxParams p, int 
     }
 }
 
-// Long runs: a block takes 256 rows of the matrix (with SwiGLU 128 gate and
-// 128 up rows) and BT routes; each of its four waves multiplies a half of
-// the rows with a half of the routes in 32 x 32 x 64 instructions, so an
-// operand byte read from LDS meets 128 or BT / 2 rows of the other.  k
-// passes in stages of 256 elements through two LDS buffers; the next
-// stage's bytes wait in registers while this one is multiplied, and are
-// written to the other buffer before the stage's last quarter is, so the
+// Long runs: a block takes 256 or 128 rows of the matrix (with SwiGLU a half
+// gate and a half up rows) and BT routes, in 32 x 32 x 64 instructions.  At BT 256 each
+// of its four waves multiplies a half of the rows with a half of the routes,
+// so an operand byte read from LDS meets 128 rows of the other.  At 128 and
+// 64 each wave multiplies a quarter of the rows with all routes, and tiles
+// of 32 routes that the run does not reach are left out: the instructions
+// follow the run's length in steps of 32.
+//
+// k passes in stages of 256 elements through two LDS buffers.  The stage
+// after the next (at BT 256, for want of registers, the next) is on its way
+// to registers while one is multiplied; the next is written from registers
+// to the other buffer before the stage's last quarter is multiplied, so the
 // matrix cores run on.
 //
 // In the 32 x 32 x 64 instruction lane l = 32 h + c holds, of row c, the 32
@@ -643,45 +663,68 @@ __global__ __launch_bounds__(kThreads, 3) void mx_stream_kernel(MxParams p, int 
 // An LDS row is the stage's 128 bytes of one operand row, eight 16-byte
 // chunks (one MX block each); chunk j lies in slot j ^ (row & 7), which
 // spreads the rows of an operand read over all banks.
-constexpr int kTileRows = 256, kStageBlocks = 8, kStageBytes = 16 * kStageBlocks;
+constexpr int kStageBlocks = 8, kStageBytes = 16 * kStageBlocks;
+// Rows of the matrix a block takes: at BT 256 as many as the registers hold
+// (two thirds of the device's rate need 128 rows for an operand byte); below,
+// where the matrix's bytes bound the kernel, few enough for two blocks on a
+// CU, so that one asks for memory while the other multiplies.
+constexpr int tile_rows(int bt) { return bt == 256 ? 256 : 128; }
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// Scale bytes of blocks b0 .. b0 + 7 of a row as two dwords; past the row's
-// last block 0.  ALIGNED: rows are whole dwords.
-template <bool ALIGNED>
-__device__ __forceinline__ uint2 load_scales(const uint8_t *row, int b0, int nblk) {
-    uint32_t v[2];
+// The scales of two stages (16 blocks) of a row, from block b0; past the
+// row's last block 0.  VEC: 16, rows are whole aligned 16-byte vectors; 4,
+// whole dwords; 1, neither.
+template <int VEC>
+__device__ __forceinline__ u32x4 load_scales(const uint8_t *row, int b0, int nblk) {
+    u32x4 v;
+    if constexpr (VEC == 16) {
+        v = *reinterpret_cast<const u32x4 *>(row + min(b0, nblk - 16));   // past the last: never read
+    } else {
 #pragma unroll
-    for (int d = 0; d < 2; ++d) {
-        const int b = b0 + 4 * d;
-        if constexpr (ALIGNED) {
-            const uint32_t t = *reinterpret_cast<const uint32_t *>(row + min(b, nblk - 4));
-            v[d] = b < nblk ? t : 0u;
-        } else {
-            v[d] = 0;
+        for (int d = 0; d < 4; ++d) {
+            const int b = b0 + 4 * d;
+            if constexpr (VEC == 4) {
+                const uint32_t t = *reinterpret_cast<const uint32_t *>(row + min(b, nblk - 4));
+                v[d] = b < nblk ? t : 0u;
+            } else {
+                v[d] = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t t = row[min(b + i, nblk - 1)];
-                v[d] |= b + i < nblk ? t << (8 * i) : 0u;
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t t = row[min(b + i, nblk - 1)];
+                    v[d] |= b + i < nblk ? t << (8 * i) : 0u;
+                }
             }
         }
     }
-    return uint2{v[0], v[1]};
+    return v;
 }
 
-template <int BT, bool SWIGLU, bool ALIGNED, typename OUT>
-__global__ __launch_bounds__(kThreads, 1) void mx_tile_kernel(MxParams p, const uint8_t *__restrict__ xc,
+// One thread's part of a stage, in registers.
+template <int WLOADS, int XLOADS> struct StagePart {
+    u32x4 w[WLOADS], x[XLOADS];
+};
+template <int N> struct Tiles {
+    static constexpr int n = N;
+};
+
+template <int BT, bool SWIGLU, int SVEC, typename OUT>
+__global__ __launch_bounds__(kThreads, BT == 256 ? 1 : 2) void mx_tile_kernel(MxParams p, const uint8_t *__restrict__ xc,
                                                               const uint8_t *__restrict__ xs,
                                                               const int32_t *__restrict__ n_runs,
                                                               const Run *__restrict__ runs,
                                                               const int32_t *__restrict__ routes, int R,
                                                               int row_tiles, OUT *__restrict__ out) {
-    constexpr int kN = 4, kT = BT / 64;              // 32-row and 32-route tiles of a wave
+    constexpr int kTileRows = tile_rows(BT);
+    constexpr int kAcross = BT == 256 ? 2 : 4;       // waves along the rows; the others along the routes
+    constexpr int kWaveRows = kTileRows / kAcross, kWaveRoutes = BT * kAcross / kWaves;
+    constexpr int kN = kWaveRows / 32, kT = kWaveRoutes / 32;
     constexpr int kWLoads = kTileRows / 32, kXLoads = BT / 32;
+    constexpr bool kFar = BT < 256;                  // two stages on their way
     __shared__ __align__(16) uint8_t wbuf[2][kTileRows * kStageBytes];
     __shared__ __align__(16) uint8_t xbuf[2][BT * kStageBytes];
-    __shared__ __align__(16) uint8_t wsc[2][kTileRows * kStageBlocks];
-    __shared__ __align__(16) uint8_t xsc[2][kTileRows * kStageBlocks];   // a row for every thread
+    // scales, two stages of all rows at a time: matrix rows, then routes
+    constexpr int kSLoads = (kTileRows + BT + kThreads - 1) / kThreads;
+    __shared__ __align__(16) uint8_t sc[2][kSLoads * kThreads][2 * kStageBlocks];
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     const int c = lane & 31, h = lane / 32;
@@ -704,12 +747,13 @@ __global__ __launch_bounds__(kThreads, 1) void mx_tile_kernel(MxParams p, const 
     const int j0 = tile * kCols;
     const int nblk = p.k / 32, stages = (nblk + kStageBlocks - 1) / kStageBlocks;
     const int64_t row_bytes = (int64_t)nblk * 16;
-    // LDS row r of the weights: with SwiGLU 64 gate rows, then their 64 up
-    // rows, for each half of the block
+    // LDS row r of the weights: with SwiGLU each wave's rows are gate rows,
+    // then the same number of up rows
     auto matrix_row = [&](int r) -> int64_t {
         if constexpr (SWIGLU) {
-            const int j = min(j0 + (r >> 7) * 64 + (r & 63), cols - 1);
-            return (int64_t)run.row * p.n + ((r & 64) ? cols : 0) + j;
+            constexpr int kHalf = kWaveRows / 2;
+            const int j = min(j0 + r / kWaveRows * kHalf + r % kHalf, cols - 1);
+            return (int64_t)run.row * p.n + (r % kWaveRows >= kHalf ? cols : 0) + j;
         } else {
             return (int64_t)run.row * p.n + min(j0 + r, cols - 1);
         }
@@ -719,7 +763,8 @@ __global__ __launch_bounds__(kThreads, 1) void mx_tile_kernel(MxParams p, const 
         return n_runs != nullptr ? routes[at] : at;
     };
 
-    const int wn = wave & 1, wt = wave >> 1;         // the wave's half of the rows, of the routes
+    const int wn = wave % kAcross, wt = wave / kAcross;
+    const int live = run.count - wt * kWaveRoutes;   // the wave's routes in the run
     f32x16 acc[kN][kT];
 #pragma unroll
     for (int i = 0; i < kN; ++i)
@@ -735,70 +780,130 @@ __global__ __launch_bounds__(kThreads, 1) void mx_tile_kernel(MxParams p, const 
         for (int i = 0; i < kWLoads; ++i) wp[i] = p.codes + matrix_row(32 * i + lr) * row_bytes;
 #pragma unroll
         for (int i = 0; i < kXLoads; ++i) xp[i] = xc + (int64_t)(route_at(32 * i + lr) / p.K) * row_bytes;
-        const uint8_t *wsp = p.scales + matrix_row(tid) * nblk;
-        const uint8_t *xsp = xs + (int64_t)(route_at(min(tid, BT - 1)) / p.K) * nblk;
-
-        u32x4 wr[kWLoads], xr[kXLoads];
-        uint2 wsr, xsr;
-        auto fetch = [&](int st) {
-            const int off = min(st * kStageBlocks + chunk, nblk - 1) * 16;
+        const uint8_t *sp[kSLoads];
 #pragma unroll
-            for (int i = 0; i < kWLoads; ++i) wr[i] = *reinterpret_cast<const u32x4 *>(wp[i] + off);
+        for (int i = 0; i < kSLoads; ++i) {
+            const int r = tid + i * kThreads;
+            sp[i] = r < kTileRows ? p.scales + matrix_row(r) * nblk
+                                  : xs + (int64_t)(route_at(min(r - kTileRows, BT - 1)) / p.K) * nblk;
+        }
+        u32x4 sr[kSLoads];
+        auto scales_fetch = [&](int g) {
 #pragma unroll
-            for (int i = 0; i < kXLoads; ++i) xr[i] = *reinterpret_cast<const u32x4 *>(xp[i] + off);
-            wsr = load_scales<ALIGNED>(wsp, st * kStageBlocks, nblk);
-            xsr = load_scales<ALIGNED>(xsp, st * kStageBlocks, nblk);
+            for (int i = 0; i < kSLoads; ++i) sr[i] = load_scales<SVEC>(sp[i], g * 2 * kStageBlocks, nblk);
         };
-        auto put = [&](int b) {
+        auto scales_put = [&](int b) {
 #pragma unroll
-            for (int i = 0; i < kWLoads; ++i) *reinterpret_cast<u32x4 *>(&wbuf[b][i * 4096 + tid * 16]) = wr[i];
-#pragma unroll
-            for (int i = 0; i < kXLoads; ++i) *reinterpret_cast<u32x4 *>(&xbuf[b][i * 4096 + tid * 16]) = xr[i];
-            *reinterpret_cast<uint2 *>(&wsc[b][tid * kStageBlocks]) = wsr;
-            *reinterpret_cast<uint2 *>(&xsc[b][tid * kStageBlocks]) = xsr;
+            for (int i = 0; i < kSLoads; ++i) *reinterpret_cast<u32x4 *>(sc[b][tid + i * kThreads]) = sr[i];
         };
-        const int r0 = wn * 128 + c, t0 = wt * (BT / 2) + c;
 
-        fetch(0);
-        put(0);
-        __syncthreads();
-        for (int st = 0; st < stages; ++st) {
-            const int b = st & 1;
-            fetch(min(st + 1, stages - 1));
-            uint32_t sa[kN], sb[kT];
+        const int r0 = wn * kWaveRows + c, t0 = wt * kWaveRoutes + c;
+        // all of k with the wave's first NT route tiles (and, kFar, the
+        // block's first 32 NT routes alone)
+        auto all_stages = [&](auto tiles) {
+            constexpr int NT = decltype(tiles)::n, kX = kFar ? NT : kXLoads;
+            using Part = StagePart<kWLoads, kX>;
+            auto fetch = [&](int st, Part &r) {      // stages past the last repeat it
+                st = min(st, stages - 1);
+                const int off = min(st * kStageBlocks + chunk, nblk - 1) * 16;
 #pragma unroll
-            for (int i = 0; i < kN; ++i)
-                sa[i] = *reinterpret_cast<const uint32_t *>(&wsc[b][(r0 + 32 * i) * kStageBlocks + 4 * h]);
+                for (int i = 0; i < kWLoads; ++i) r.w[i] = *reinterpret_cast<const u32x4 *>(wp[i] + off);
 #pragma unroll
-            for (int i = 0; i < kT; ++i)
-                sb[i] = *reinterpret_cast<const uint32_t *>(&xsc[b][(t0 + 32 * i) * kStageBlocks + 4 * h]);
+                for (int i = 0; i < kX; ++i) r.x[i] = *reinterpret_cast<const u32x4 *>(xp[i] + off);
+            };
+            auto put = [&](int b, const Part &r) {
+#pragma unroll
+                for (int i = 0; i < kWLoads; ++i)
+                    *reinterpret_cast<u32x4 *>(&wbuf[b][i * 4096 + tid * 16]) = r.w[i];
+#pragma unroll
+                for (int i = 0; i < kX; ++i) *reinterpret_cast<u32x4 *>(&xbuf[b][i * 4096 + tid * 16]) = r.x[i];
+            };
+            // stage st, from buffer B = st & 1; `next` (the stage after) goes
+            // to the other buffer, which nobody has read since the last
+            // barrier, and so do the next two stages' scales in every second
+            auto stage = [&](int b, int st, const Part &next) {
+                const int g = (st >> 1) & 1;
+                uint32_t sa[kN], sb[NT];
+#pragma unroll
+                for (int i = 0; i < kN; ++i)
+                    sa[i] = *reinterpret_cast<const uint32_t *>(&sc[g][r0 + 32 * i][kStageBlocks * b + 4 * h]);
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    sb[i] = *reinterpret_cast<const uint32_t *>(
+                        &sc[g][kTileRows + t0 + 32 * i][kStageBlocks * b + 4 * h]);
 #define MOE_READ(S)                                                                                       \
-    u32x4 wa##S[kN], xb##S[kT];                                                                           \
+    u32x4 wa##S[kN], xb##S[NT];                                                                           \
     {                                                                                                     \
         const int slot = ((4 * h + S) ^ (c & 7)) * 16;                                                    \
-        _Pragma("unroll") for (int i = 0; i < kT; ++i) xb##S[i] =                                         \
+        _Pragma("unroll") for (int i = 0; i < NT; ++i) xb##S[i] =                                         \
             *reinterpret_cast<const u32x4 *>(&xbuf[b][(t0 + 32 * i) * kStageBytes + slot]);               \
         _Pragma("unroll") for (int i = 0; i < kN; ++i) wa##S[i] =                                         \
             *reinterpret_cast<const u32x4 *>(&wbuf[b][(r0 + 32 * i) * kStageBytes + slot]);               \
     }
 #define MOE_MULTIPLY(S)                                                                                   \
-    _Pragma("unroll") for (int i = 0; i < kN; ++i) _Pragma("unroll") for (int j = 0; j < kT; ++j)         \
+    _Pragma("unroll") for (int i = 0; i < kN; ++i) _Pragma("unroll") for (int j = 0; j < NT; ++j)         \
         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                                      \
             widen(wa##S[i]), widen(xb##S[j]), acc[i][j], kFp4, kFp4, S, (int)sa[i], S, (int)sb[j]);
-            MOE_READ(0)
-            MOE_READ(1)
-            MOE_MULTIPLY(0)
-            MOE_READ(2)
-            MOE_MULTIPLY(1)
-            MOE_READ(3)
-            MOE_MULTIPLY(2)
-            __builtin_amdgcn_sched_barrier(0);
-            put(b ^ 1);   // read by nobody since the last barrier
-            __builtin_amdgcn_sched_barrier(0);
-            MOE_MULTIPLY(3)
+                MOE_READ(0)
+                MOE_READ(1)
+                MOE_MULTIPLY(0)
+                MOE_READ(2)
+                MOE_MULTIPLY(1)
+                MOE_READ(3)
+                MOE_MULTIPLY(2)
+                __builtin_amdgcn_sched_barrier(0);
+                put(b ^ 1, next);
+                if (!kFar || b == 1) scales_put(g ^ 1);
+                __builtin_amdgcn_sched_barrier(0);
+                MOE_MULTIPLY(3)
 #undef MOE_READ
 #undef MOE_MULTIPLY
-            __syncthreads();
+                lds_barrier();
+            };
+
+            scales_fetch(0);
+            if constexpr (kFar) {
+                Part even, odd;
+                fetch(0, even);
+                fetch(1, odd);
+                scales_put(0);
+                put(0, even);
+                lds_barrier();
+                for (int st = 0; st < stages; st += 2) {
+                    scales_fetch((st >> 1) + 1);
+                    fetch(st + 2, even);
+                    stage(0, st, odd);
+                    if (st + 1 >= stages) break;
+                    fetch(st + 3, odd);
+                    stage(1, st + 1, even);
+                }
+            } else {
+                // (two copies of the stage would not fit the registers: the
+                // scales are fetched and put again in the second)
+                Part next;
+                fetch(0, next);
+                scales_put(0);
+                put(0, next);
+                lds_barrier();
+                for (int st = 0; st < stages; ++st) {
+                    scales_fetch((st >> 1) + 1);
+                    fetch(st + 1, next);
+                    stage(st & 1, st, next);
+                }
+            }
+        };
+        if constexpr (kFar) {
+            static_assert(kT <= 4, "route tiles of a wave");
+            if (live > 96)
+                all_stages(Tiles<kT>{});
+            else if (live > 64)
+                all_stages(Tiles<(kT < 3 ? kT : 3)>{});
+            else if (live > 32)
+                all_stages(Tiles<2>{});
+            else
+                all_stages(Tiles<1>{});
+        } else {
+            all_stages(Tiles<kT>{});
         }
     }
 
@@ -806,22 +911,25 @@ __global__ __launch_bounds__(kThreads, 1) void mx_tile_kernel(MxParams p, const 
     const bool whole = cols % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (4 * sizeof(OUT) - 1)) == 0;
 #pragma unroll
     for (int j = 0; j < kT; ++j) {
-        const int at = wt * (BT / 2) + 32 * j + c;
+        const int at = wt * kWaveRoutes + 32 * j + c;
         if (at >= run.count) continue;
         OUT *o = out + (int64_t)route_at(at) * cols;
+        // groups of four rows: 4 kN of them, with SwiGLU the first half gate, the second up
+        constexpr int kGroups = SWIGLU ? 2 * kN : 4 * kN;
 #pragma unroll
-        for (int i = 0; i < (SWIGLU ? kN / 2 : kN); ++i)
+        for (int g = 0; g < kGroups; ++g) {
+            const int col = j0 + wn * (kCols / kAcross) + 8 * g + 4 * h;
+            f32x4 v;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int col = j0 + wn * (kCols / 2) + 32 * i + 8 * g + 4 * h;
-                f32x4 v;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[e] = acc[i][j][4 * g + e];
-                    if constexpr (SWIGLU) v[e] = silu(v[e]) * acc[i + kN / 2][j][4 * g + e];
+            for (int e = 0; e < 4; ++e) {
+                v[e] = acc[g / 4][j][4 * (g % 4) + e];
+                if constexpr (SWIGLU) {
+                    constexpr int kUp = 2 * kN;
+                    v[e] = silu(v[e]) * acc[(g + kUp) / 4][j][4 * ((g + kUp) % 4) + e];
                 }
-                store4(o, col, cols, whole, v);
             }
+            store4(o, col, cols, whole, v);
+        }
     }
 }
 
@@ -888,21 +996,26 @@ hipError_t launch_stream(const MxParams &p, int mode, const int32_t *n_runs, con
 template <int BT, typename OUT>
 hipError_t launch_tile(const MxParams &p, const uint8_t *xc, const uint8_t *xs, const int32_t *n_runs,
                        const Run *runs, const int32_t *routes, int R, int64_t max_runs, hipStream_t s) {
-    const int per = p.swiglu ? kTileRows / 2 : kTileRows, cols = p.swiglu ? p.n / 2 : p.n;
+    const int per = p.swiglu ? tile_rows(BT) / 2 : tile_rows(BT), cols = p.swiglu ? p.n / 2 : p.n;
     const int row_tiles = (cols + per - 1) / per;
     const unsigned grid = (unsigned)((max_runs * row_tiles + 7) / 8 * 8);
-    const bool aligned = p.k % 128 == 0 && reinterpret_cast<uintptr_t>(p.scales) % 4 == 0;
-#define MOE_TILE(S, A)                                                                                          \
-    hipLaunchKernelGGL((mx_tile_kernel<BT, S, A, OUT>), dim3(grid), dim3(kThreads), 0, s, p, xc, xs, n_runs, runs, \
+    const uintptr_t sp = reinterpret_cast<uintptr_t>(p.scales);
+#define MOE_TILE(S, V)                                                                                          \
+    hipLaunchKernelGGL((mx_tile_kernel<BT, S, V, OUT>), dim3(grid), dim3(kThreads), 0, s, p, xc, xs, n_runs, runs, \
                        routes, R, row_tiles, static_cast<OUT *>(p.out))
-    if (p.swiglu && aligned)
-        MOE_TILE(true, true);
-    else if (p.swiglu)
-        MOE_TILE(true, false);
-    else if (aligned)
-        MOE_TILE(false, true);
-    else
-        MOE_TILE(false, false);
+#define MOE_TILE_S(S)                        \
+    if (p.k % 512 == 0 && sp % 16 == 0)      \
+        MOE_TILE(S, 16);                     \
+    else if (p.k % 128 == 0 && sp % 4 == 0)  \
+        MOE_TILE(S, 4);                      \
+    else                                     \
+        MOE_TILE(S, 1);
+    if (p.swiglu) {
+        MOE_TILE_S(true)
+    } else {
+        MOE_TILE_S(false)
+    }
+#undef MOE_TILE_S
 #undef MOE_TILE
     return hipGetLastError();
 }
