@@ -18,10 +18,12 @@
 // nothing in any sum (fp32 reaches down to 2^-149).
 #include <algorithm>
 
-#include "moe_internal.h"
+#include "k_rows.inc"
 
 namespace moe {
 namespace {
+
+using namespace rows_detail;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -103,7 +105,10 @@ MxWs mx_ws(int P, int k, int T, int K) {
 // of at most run_length routes.  Routes without a row sort behind the last
 // row, as runs of row -1.  The order inside a list is not fixed; every
 // route's result is independent of its place.
-constexpr int kGroupThreads = 1024, kGroupWaves = kGroupThreads / kWave;
+constexpr int kGroupThreads = 1024, kGroupWaves = kGroupThreads / kWave, kGroupAhead = 8;
+// LDS of the list-making block: counters of up to 32769 rows (131 KB), or
+// fewer and the sorted ids.
+constexpr int kPrepareLds = 144 << 10;
 
 // The next free place of `row`, one for each active lane.  Lanes that share
 // the first lane's row take theirs with one addition (one matrix for all
@@ -118,21 +123,59 @@ __device__ __forceinline__ int place(int32_t *cnt, int row) {
     return __builtin_amdgcn_readfirstlane(base) + before;
 }
 
-__global__ __launch_bounds__(kGroupThreads) void mx_group_kernel(const int32_t *__restrict__ idx, int R, int P,
-                                                                 int run_length, int32_t *__restrict__ n_runs,
-                                                                 Run *__restrict__ runs,
-                                                                 int32_t *__restrict__ routes) {
+// Block 0 makes the lists; the others, if any, quantise x, so the one goes on
+// beside the other.  lists = 0: every block quantises.  staged: the sorted
+// ids are put together in LDS and written in order (a scattered store of 64
+// lanes takes 64 turns: 24576 ids 24 -> 12 us), where they fit.
+struct PrepareParams {
+    const int32_t *idx;
+    int32_t R, P, run_length, lists, staged;
+    int32_t *n_runs;
+    Run *runs;
+    int32_t *routes;
+    const uint16_t *x;
+    int64_t x_stride, units;             // of 8 elements
+    int32_t upr;
+    FastDiv by_upr;
+    uint8_t *codes, *scales;
+};
+
+template <bool VEC>
+__global__ __launch_bounds__(kGroupThreads) void mx_prepare_kernel(PrepareParams a) {
     extern __shared__ __align__(16) int32_t lds[];
-    int32_t *wsum = lds;         // [2][kGroupWaves]
-    int32_t *cnt = lds + 2 * kGroupWaves;   // [P + 1]
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    if ((int)blockIdx.x >= a.lists) {
+        const int64_t step = (int64_t)(gridDim.x - a.lists) * kGroupThreads;
+        for (int64_t u = (int64_t)(blockIdx.x - a.lists) * kGroupThreads + tid; u < a.units; u += step) {
+            const int64_t row = (int64_t)a.by_upr((uint64_t)u);
+            float f[kPer];
+            load8<VEC>(a.x + row * a.x_stride + (u - row * a.upr) * kPer, f);
+            uint32_t sc;
+            const uint32_t c = mx_codes(f, quad_max(amax_bits(f)), sc);
+            reinterpret_cast<uint32_t *>(a.codes)[u] = c;
+            if ((tid & 3) == 0) a.scales[u / 4] = (uint8_t)sc;
+        }
+        return;
+    }
+    const int R = a.R, P = a.P, run_length = a.run_length;
+    int32_t *wsum = lds;                    // [2][kGroupWaves]
+    int32_t *cnt = lds + 2 * kGroupWaves;   // [P + 1]
+    int32_t *sorted = cnt + P + 1;          // [R], staged
     for (int r = tid; r <= P; r += kGroupThreads) cnt[r] = 0;
     __syncthreads();
-    for (int i = tid; i < R; i += kGroupThreads) {
-        const int r = idx[i];
-        const int row = r >= 0 && r < P ? r : P;
-        place(cnt, row);
-    }
+    // eight ids of a thread at a time are on their way together
+    auto each = [&](auto visit) {
+        for (int i0 = tid; i0 < R; i0 += kGroupAhead * kGroupThreads) {
+            int r[kGroupAhead];
+#pragma unroll
+            for (int k = 0; k < kGroupAhead; ++k) r[k] = a.idx[min(i0 + k * kGroupThreads, R - 1)];
+#pragma unroll
+            for (int k = 0; k < kGroupAhead; ++k)
+                if (i0 + k * kGroupThreads < R)
+                    visit(i0 + k * kGroupThreads, r[k] >= 0 && r[k] < P ? r[k] : P);
+        }
+    };
+    each([&](int, int row) { place(cnt, row); });
     __syncthreads();
     const int per = (P + kGroupThreads) / kGroupThreads;   // rows 0..P
     const int r0 = tid * per;
@@ -160,15 +203,17 @@ __global__ __launch_bounds__(kGroupThreads) void mx_group_kernel(const int32_t *
             const int v = cnt[r0 + i];
             cnt[r0 + i] = start;
             for (int o = 0; o < v; o += run_length)
-                runs[run++] = Run{r0 + i < P ? r0 + i : -1, start + o, min(run_length, v - o), 0};
+                a.runs[run++] = Run{r0 + i < P ? r0 + i : -1, start + o, min(run_length, v - o), 0};
             start += v;
         }
-    if (tid == 0) n_runs[0] = total;
+    if (tid == 0) a.n_runs[0] = total;
     __syncthreads();
-    for (int i = tid; i < R; i += kGroupThreads) {
-        const int r = idx[i];
-        const int row = r >= 0 && r < P ? r : P;
-        routes[place(cnt, row)] = i;
+    if (a.staged) {
+        each([&](int i, int row) { sorted[place(cnt, row)] = i; });
+        __syncthreads();
+        for (int i = tid; i < R; i += kGroupThreads) a.routes[i] = sorted[i];
+    } else {
+        each([&](int i, int row) { a.routes[place(cnt, row)] = i; });
     }
 }
 
@@ -1053,31 +1098,51 @@ hipError_t launch_mx_product(const MxParams &p, bool reuse_lists, hipStream_t s)
         return launch_stream(p, by_route ? kByRoute : kByRow, nullptr, nullptr, nullptr, R,
                              by_route ? R : p.P + 1, s);
     }
-    hipError_t e = hipSuccess;
-    int64_t max_runs = (R + run_length - 1) / run_length;
-    if (p.idx != nullptr) {
-        max_runs = std::min<int64_t>(R, (int64_t)p.P + 1) + R / run_length;
-        if (!reuse_lists) {
-            const size_t lds = (2 * kGroupWaves + (size_t)p.P + 1) * 4;
-            if (lds > 65536) {
-                e = hipFuncSetAttribute(reinterpret_cast<const void *>(&mx_group_kernel),
-                                        hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-                if (e != hipSuccess) return e;
-            }
-            hipLaunchKernelGGL(mx_group_kernel, dim3(1), dim3(kGroupThreads), lds, s, p.idx, R, p.P, run_length,
-                               n_runs, runs, routes);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
+    // lists of routes, and x quantised where a tile kernel reads it
+    const int lists = p.idx != nullptr && !reuse_lists;
+    if (lists || !stream) {
+        PrepareParams a{.idx = p.idx,
+                        .R = R,
+                        .P = p.P,
+                        .run_length = run_length,
+                        .lists = lists,
+                        .staged = 0,
+                        .n_runs = n_runs,
+                        .runs = runs,
+                        .routes = routes,
+                        .x = p.x,
+                        .x_stride = p.x_stride,
+                        .units = stream ? 0 : (int64_t)p.T * (p.k / kPer),
+                        .upr = p.k / kPer,
+                        .by_upr = FastDiv((uint64_t)p.k / kPer),
+                        .codes = xc,
+                        .scales = xs};
+        size_t lds = lists ? (2 * kGroupWaves + (size_t)p.P + 1) * 4 : 0;
+        if (lists && lds + (size_t)R * 4 <= kPrepareLds) {
+            a.staged = 1;
+            lds += (size_t)R * 4;
         }
-    } else {
-        n_runs = nullptr;
+        const bool vec = vector_rows(p.x, p.x_stride, p.T, 2);
+        const void *fn = vec ? reinterpret_cast<const void *>(&mx_prepare_kernel<true>)
+                             : reinterpret_cast<const void *>(&mx_prepare_kernel<false>);
+        if (lds > 65536) {
+            hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, kPrepareLds);
+            if (e != hipSuccess) return e;
+        }
+        const unsigned grid = lists + (unsigned)std::min<int64_t>((a.units + kGroupThreads - 1) / kGroupThreads, 4096);
+        if (vec)
+            hipLaunchKernelGGL(mx_prepare_kernel<true>, dim3(grid), dim3(kGroupThreads), lds, s, a);
+        else
+            hipLaunchKernelGGL(mx_prepare_kernel<false>, dim3(grid), dim3(kGroupThreads), lds, s, a);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
+    int64_t max_runs = (R + run_length - 1) / run_length;
+    if (p.idx != nullptr)
+        max_runs = std::min<int64_t>(R, (int64_t)p.P + 1) + R / run_length;
+    else
+        n_runs = nullptr;
     if (stream) return launch_stream(p, kRuns, n_runs, runs, routes, R, max_runs, s);
-    RowsParams rp{};
-    rp.rows = p.T;
-    rp.cols = p.k;
-    rp.stride = p.x_stride;
-    e = launch_quantize(MOE_FMT_MXFP4, MOE_TYPE_BF16, rp, p.x, xc, xs, s);
-    if (e != hipSuccess) return e;
     return p.out_type == MOE_TYPE_F32
                ? launch_tile_for<float>(run_length, p, xc, xs, n_runs, runs, routes, R, max_runs, s)
                : launch_tile_for<uint16_t>(run_length, p, xc, xs, n_runs, runs, routes, R, max_runs, s);

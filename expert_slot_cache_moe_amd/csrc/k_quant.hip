@@ -1,63 +1,25 @@
 // Rows of floats to the 4-bit bank formats, and back.
 //
 // One pass: a lane holds 8 consecutive elements, the 4 (MXFP4) or 2 (E2M1)
-// lanes of a block share their largest magnitude through DPP lane moves,
-// and each lane writes its 8 codes as one dword.
+// lanes of a block share their largest magnitude, and each lane writes its 8
+// codes as one dword.
 //
-// MXFP4 scales are powers of two, so x / scale is exact and the hardware's
-// scaled conversion rounds it (to nearest, ties to the even code,
-// saturating).  E2M1 scales are not: x / (scale g) is rounded wherever it
+// MXFP4 scales are powers of two, so x / scale is exact and rounded once, by
+// the hardware's scaled conversion.  E2M1 scales are not: x / (scale g) is rounded wherever it
 // is formed, and a value next to the middle of two codes could cross it.
 // The middles m scale g have at most 31 significant bits (m 3, scale 4, g
 // 24) and x at most 24, so a quotient that is not exactly a middle differs
 // from it by more than 2^-32 of its size: a 53-bit quotient tells the two
 // apart, and is handed to the conversion with its tail folded into the last
 // fp32 bit.
-#include "moe_internal.h"
+#include "k_rows.inc"
 
 namespace moe {
 namespace {
 
+using namespace rows_detail;
+
 constexpr int kThreads = 256;
-constexpr int kPer = 8;   // elements per lane
-
-// q = u / d for u d < 2^64, magic = ceil(2^64 / d), d > 1; d = 1 has magic 0.
-struct FastDiv {
-    uint64_t magic;
-    __host__ explicit FastDiv(uint64_t d) : magic(d <= 1 ? 0 : ~0ull / d + 1) {}
-    __device__ __forceinline__ uint64_t operator()(uint64_t u) const {
-        return magic ? __umul64hi(u, magic) : u;
-    }
-};
-
-// Lane moves inside a quad: the other lane of a pair, the other pair.
-constexpr int kDppPair = 0xB1, kDppQuad = 0x4E;   // quad_perm [1,0,3,2], [2,3,0,1]
-template <int CTRL> __device__ __forceinline__ uint32_t quad_move(uint32_t x) {
-    return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xf, 0xf, true);
-}
-
-// Eight elements as fp32, by whole vectors or one at a time.
-template <bool VEC> __device__ __forceinline__ void load8(const float *p, float (&f)[kPer]) {
-    if constexpr (VEC) {
-        const u32x4 a = reinterpret_cast<const u32x4 *>(p)[0], b = reinterpret_cast<const u32x4 *>(p)[1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(a[i]), f[4 + i] = __uint_as_float(b[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) f[i] = p[i];
-    }
-}
-template <bool VEC> __device__ __forceinline__ void load8(const uint16_t *p, float (&f)[kPer]) {
-    if constexpr (VEC) {
-        const u32x4 a = *reinterpret_cast<const u32x4 *>(p);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(a[i]), f[2 * i + 1] = bf16_hi(a[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) f[i] = bf16_f(p[i]);
-    }
-}
-
 // x inv to fp32 for the E2M1 conversion: cut to 24 bits, with the last bit
 // set where more was cut than the quotient's own error.  inv carries a
 // factor 1 + 2^-50, above every rounding in it (3 x 2^-53), so an exact
@@ -93,41 +55,27 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const SRC *__restric
         const int64_t row = (int64_t)by_upr((uint64_t)u);
         float f[kPer];
         load8<VEC>(src + row * stride + (u - row * upr) * kPer, f);
-        uint32_t a = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) a = max(a, __float_as_uint(f[i]) & 0x7fffffffu);
-        a = max(a, quad_move<kDppPair>(a));
-        if constexpr (FMT == MOE_FMT_MXFP4) a = max(a, quad_move<kDppQuad>(a));
-        bool bad = a >= 0x7f800000u;
-        uint32_t sc;
-        float q[kPer];
+        uint32_t a = amax_bits(f), sc, c = 0;
         if constexpr (FMT == MOE_FMT_MXFP4) {
-            sc = (uint32_t)max((int)(a >> 23) - 2, 0);
-            // x 2^(127 - sc), exact (a quotient is at most 8); in two
-            // factors, each a normal float
-            const int up = 127 - (int)sc;
-            const float m0 = __uint_as_float((uint32_t)(127 + up / 2) << 23),
-                        m1 = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) q[i] = f[i] * m0 * m1;
-            if (bad) sc = 0xFF;
+            c = mx_codes(f, quad_max(a), sc);
         } else {
+            a = pair_max(a);
             const float g = globals ? globals[by_global((uint64_t)row)] : 1.f;
-            bad |= !(g > 0.f && g < INFINITY);
+            bool bad = a >= 0x7f800000u || !(g > 0.f && g < INFINITY);
             sc = bad ? 0x7Fu : e4m3_of((double)__uint_as_float(a) / (6.0 * (double)g));
             bad |= sc == 0;   // scale 0: codes 0
             const double inv = bad ? 0.0 : 1.0 / ((double)e4m3_f(sc) * (double)g) * (1.0 + 0x1p-50);
+            if (!bad) {
+                float q[kPer];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) q[i] = __builtin_amdgcn_fmed3f(quotient(f[i], inv), -8.f, 8.f);
-        }
-        uint32_t c = 0;
-        if (!bad) {
+                for (int i = 0; i < kPer; ++i) q[i] = __builtin_amdgcn_fmed3f(quotient(f[i], inv), -8.f, 8.f);
 #define MOE_CVT(B) c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, q[2 * B], q[2 * B + 1], 1.0f, B);
-            MOE_CVT(0)
-            MOE_CVT(1)
-            MOE_CVT(2)
-            MOE_CVT(3)
+                MOE_CVT(0)
+                MOE_CVT(1)
+                MOE_CVT(2)
+                MOE_CVT(3)
 #undef MOE_CVT
+            }
         }
         reinterpret_cast<uint32_t *>(codes)[u] = c;
         if ((threadIdx.x & (kLanes - 1)) == 0) scales[u / kLanes] = (uint8_t)sc;
@@ -200,11 +148,6 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t *__r
 int grid_for(int64_t units) {
     const int64_t blocks = (units + kThreads - 1) / kThreads;
     return (int)(blocks < 65536 ? blocks : 65536);
-}
-
-// Whole-vector access to the dense rows: every row starts on 16 bytes.
-bool vector_rows(const void *p, int64_t stride, int64_t rows, int bytes) {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (rows <= 1 || (stride * bytes) % 16 == 0);
 }
 
 }  // namespace
