@@ -1114,7 +1114,7 @@ hipError_t launch_mx_product(const MxParams &p, bool reuse_lists, hipStream_t s)
                         .x_stride = p.x_stride,
                         .units = stream ? 0 : (int64_t)p.T * (p.k / kPer),
                         .upr = p.k / kPer,
-                        .by_upr = FastDiv((uint64_t)p.k / kPer),
+                        .by_upr = FastDiv((uint64_t)p.k / kPer, (uint64_t)p.T * (p.k / kPer)),
                         .codes = xc,
                         .scales = xs};
         size_t lds = lists ? (2 * kGroupWaves + (size_t)p.P + 1) * 4 : 0;

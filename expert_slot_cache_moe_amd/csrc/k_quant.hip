@@ -1,17 +1,20 @@
 // Rows of floats to the 4-bit bank formats, and back.
 //
-// One pass: a lane holds 8 consecutive elements, the 4 (MXFP4) or 2 (E2M1)
-// lanes of a block share their largest magnitude, and each lane writes its 8
-// codes as one dword.
+// One pass: an MXFP4 lane holds 8 consecutive elements, and the 4 lanes of a
+// block share their largest magnitude; an E2M1 lane holds a block of 16.
 //
 // MXFP4 scales are powers of two, so x / scale is exact and rounded once, by
-// the hardware's scaled conversion.  E2M1 scales are not: x / (scale g) is rounded wherever it
-// is formed, and a value next to the middle of two codes could cross it.
-// The middles m scale g have at most 31 significant bits (m 3, scale 4, g
-// 24) and x at most 24, so a quotient that is not exactly a middle differs
-// from it by more than 2^-32 of its size: a 53-bit quotient tells the two
-// apart, and is handed to the conversion with its tail folded into the last
-// fp32 bit.
+// the hardware's scaled conversion.  E2M1 scales are not: x / (scale g) is
+// rounded wherever it is formed, and a value next to the middle of two codes
+// could cross it.  The middles m scale g have at most 31 significant bits (m
+// 3, scale 4, g 24) and x at most 24, so a quotient that is not exactly a
+// middle differs from it by more than 2^-32 of its size.  A quotient of two
+// fp32 parts tells the two apart; it is handed to the conversion rounded to
+// odd, which keeps what lies off a middle off it.  The same holds for the
+// scale itself, a / (6 g) against the middles of E4M3.
+//
+// Bound by memory: a 134M element bf16 matrix to MXFP4 takes 70 us on
+// MI355X (4.9 TB/s, a large copy's rate), to E2M1 79 us; back, 76 us.
 #include "k_rows.inc"
 
 namespace moe {
@@ -20,18 +23,21 @@ namespace {
 using namespace rows_detail;
 
 constexpr int kThreads = 256;
+
+// ---- any g: quotients in 64 bits
+
 // x inv to fp32 for the E2M1 conversion: cut to 24 bits, with the last bit
 // set where more was cut than the quotient's own error.  inv carries a
 // factor 1 + 2^-50, above every rounding in it (3 x 2^-53), so an exact
 // middle lands on itself and up to 2^-49 above, never below; the tail below
 // 2^-44 counts as nothing.
-__device__ __forceinline__ float quotient(float x, double inv) {
+__device__ __forceinline__ float quotient64(float x, double inv) {
     const double y = (double)x * inv;
     uint64_t u = (uint64_t)__double_as_longlong(y);
     const uint32_t tail = (uint32_t)u & 0x1fffffffu;   // the 29 bits below fp32's last
     u &= ~0x1fffffffull;
     if (tail >= (1u << 8)) u |= 0x20000000u;
-    return (float)__longlong_as_double((long long)u);
+    return __builtin_amdgcn_fmed3f((float)__longlong_as_double((long long)u), -8.f, 8.f);
 }
 
 // E4M3 byte of v >= 0: nearest, ties to even, at most 448.
@@ -43,56 +49,142 @@ __device__ __forceinline__ uint32_t e4m3_of(double v) {
     return (uint32_t)((e + 6) * 8 + (int)q);
 }
 
-template <int FMT, bool VEC, typename SRC>
-__global__ __launch_bounds__(kThreads) void quantize_kernel(const SRC *__restrict__ src, int64_t stride,
-                                                            int64_t units, int upr, FastDiv by_upr,
-                                                            const float *__restrict__ globals,
-                                                            FastDiv by_global, uint8_t *__restrict__ codes,
-                                                            uint8_t *__restrict__ scales) {
-    constexpr int kLanes = FMT == MOE_FMT_MXFP4 ? 4 : 2;   // lanes per block
+// ---- g of ordinary size (2^-80 to 2^80): the same in pairs of fp32, which
+// took the 134M element matrix from 127 to 79 us
+
+// E4M3 byte of a / (6 g): a candidate from an approximate quotient, moved up
+// where a lies above the middle over it (or on it, and the candidate is
+// odd).  6 g = hi + lo exactly, and a - middle hi is exact wherever it is
+// small enough for middle lo to matter, so the comparison is exact.
+__device__ __forceinline__ uint32_t e4m3_of(float a, float g) {
+    const float hi = 6.f * g, lo = fmaf(6.f, g, -hi);
+    const float t = a * __builtin_amdgcn_rcpf(hi);
+    if (t >= 470.f) return 0x7E;
+    const int e = max((int)(__float_as_uint(t) >> 23) - 127, -6);
+    const int k = (int)floorf(ldexpf(t, 3 - e));
+    const float middle = ldexpf((float)k + 0.5f, e - 3);
+    const float over = fmaf(-middle, lo, fmaf(-middle, hi, a));
+    const int q = k + (over > 0.f || (over == 0.f && (k & 1)));
+    return (uint32_t)min((e + 6) * 8 + q, 0x7E);
+}
+
+// The reciprocal of s g (a scale of 4 bits, g of 24) in two parts.  TRIM: the
+// first part has 16 bits, so that its product with a bf16 number is exact.
+template <bool TRIM> __device__ __forceinline__ void reciprocal(float s, float g, float &ih, float &il) {
+    const float uh = s * g, ul = fmaf(s, g, -uh);
+    float r = __builtin_amdgcn_rcpf(uh);
+    r = fmaf(r, fmaf(-uh, r, 1.f), r);
+    ih = TRIM ? __uint_as_float(__float_as_uint(r) & 0xffffff00u) : r;
+    il = fmaf(-ul, ih, fmaf(-uh, ih, 1.f)) * r;
+}
+
+// x (ih + il) rounded to odd: the nearest fp32 p, its last bit set (and one
+// taken off first, where the quotient is smaller) unless the rest is none.
+// The two parts are good to 2^-39 of a quotient, of at most 5 where it
+// matters: a rest below 2^-36 is none, and what is off a middle is off by at
+// least 2^-33.
+template <bool TRIM> __device__ __forceinline__ float quotient(float x, float ih, float il) {
+    const float ax = fabsf(x);
+    float p = fminf(ax * ih, 16.f), rest;     // the largest code is 6
+    if constexpr (TRIM) {
+        const float p0 = p;                   // exact
+        p = fmaf(ax, il, p0);
+        rest = fmaf(ax, il, p0 - p);
+    } else {
+        const float p0 = p, r0 = fmaf(ax, il, fmaf(ax, ih, -p0));
+        p = p0 + r0;
+        rest = r0 - (p - p0);
+    }
+    const uint32_t u = __float_as_uint(p);
+    const uint32_t odd = (u + (uint32_t)((int)__float_as_uint(rest) >> 31)) | 1u;
+    const uint32_t v = fabsf(rest) > 0x1p-35f ? odd : u;
+    return __uint_as_float(v | (__float_as_uint(x) & 0x80000000u));
+}
+
+// MXFP4: eight elements a lane.
+template <bool VEC, typename SRC>
+__global__ __launch_bounds__(kThreads) void quantize_mx_kernel(const SRC *__restrict__ src, int64_t stride,
+                                                               int64_t units, int upr, FastDiv by_upr,
+                                                               uint8_t *__restrict__ codes,
+                                                               uint8_t *__restrict__ scales) {
     const int64_t step = (int64_t)gridDim.x * kThreads;
     for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units; u += step) {
         const int64_t row = (int64_t)by_upr((uint64_t)u);
         float f[kPer];
         load8<VEC>(src + row * stride + (u - row * upr) * kPer, f);
-        uint32_t a = amax_bits(f), sc, c = 0;
-        if constexpr (FMT == MOE_FMT_MXFP4) {
-            c = mx_codes(f, quad_max(a), sc);
-        } else {
-            a = pair_max(a);
-            const float g = globals ? globals[by_global((uint64_t)row)] : 1.f;
-            bool bad = a >= 0x7f800000u || !(g > 0.f && g < INFINITY);
-            sc = bad ? 0x7Fu : e4m3_of((double)__uint_as_float(a) / (6.0 * (double)g));
-            bad |= sc == 0;   // scale 0: codes 0
-            const double inv = bad ? 0.0 : 1.0 / ((double)e4m3_f(sc) * (double)g) * (1.0 + 0x1p-50);
-            if (!bad) {
-                float q[kPer];
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) q[i] = __builtin_amdgcn_fmed3f(quotient(f[i], inv), -8.f, 8.f);
-#define MOE_CVT(B) c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, q[2 * B], q[2 * B + 1], 1.0f, B);
-                MOE_CVT(0)
-                MOE_CVT(1)
-                MOE_CVT(2)
-                MOE_CVT(3)
-#undef MOE_CVT
-            }
-        }
+        uint32_t sc;
+        const uint32_t c = mx_codes(f, quad_max(amax_bits(f)), sc);
         reinterpret_cast<uint32_t *>(codes)[u] = c;
-        if ((threadIdx.x & (kLanes - 1)) == 0) scales[u / kLanes] = (uint8_t)sc;
+        if ((threadIdx.x & 3) == 0) scales[u / 4] = (uint8_t)sc;
     }
 }
 
-// code * scale * g rounded once to bf16: the fp32 product rounded first
-// could land on a bf16 middle it is not on; its error (exact, by fma) then
-// says to which side it belongs.
-__device__ __forceinline__ uint16_t bf16_once(float a, float g) {
+// E2M1: a block of 16 a lane, so that its scale and reciprocal are made once.
+template <bool VEC, typename SRC>
+__global__ __launch_bounds__(kThreads) void quantize_e2m1_kernel(const SRC *__restrict__ src, int64_t stride,
+                                                                 int64_t units, int upr, FastDiv by_upr,
+                                                                 const float *__restrict__ globals,
+                                                                 FastDiv by_global, uint8_t *__restrict__ codes,
+                                                                 uint8_t *__restrict__ scales) {
+    constexpr bool kTrim = sizeof(SRC) == 2;
+    const int64_t step = (int64_t)gridDim.x * kThreads;
+    for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units; u += step) {
+        const int64_t row = (int64_t)by_upr((uint64_t)u);
+        const SRC *p = src + row * stride + (u - row * upr) * 2 * kPer;
+        float f[2][kPer];
+        load8<VEC>(p, f[0]);
+        load8<VEC>(p + kPer, f[1]);
+        const float g = globals ? globals[by_global((uint64_t)row)] : 1.f;
+        const uint32_t a = max(amax_bits(f[0]), amax_bits(f[1]));
+        bool bad = a >= 0x7f800000u || !(g > 0.f && g < INFINITY);
+        uint32_t sc;
+        float q[2][kPer];
+        if (g >= 0x1p-80f && g <= 0x1p80f) {
+            sc = bad ? 0x7Fu : e4m3_of(__uint_as_float(a), g);
+            float ih, il;
+            reciprocal<kTrim>(e4m3_f(sc), g, ih, il);
+#pragma unroll
+            for (int i = 0; i < 2 * kPer; ++i) q[i / kPer][i % kPer] = quotient<kTrim>(f[i / kPer][i % kPer], ih, il);
+        } else {
+            sc = bad ? 0x7Fu : e4m3_of((double)__uint_as_float(a) / (6.0 * (double)g));
+            const double inv = 1.0 / ((double)e4m3_f(sc) * (double)g) * (1.0 + 0x1p-50);
+#pragma unroll
+            for (int i = 0; i < 2 * kPer; ++i) q[i / kPer][i % kPer] = quotient64(f[i / kPer][i % kPer], inv);
+        }
+        bad |= sc == 0;   // scale 0: codes 0
+        uint32_t c[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#define MOE_CVT(B) c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c[i], q[i][2 * B], q[i][2 * B + 1], 1.0f, B);
+            MOE_CVT(0)
+            MOE_CVT(1)
+            MOE_CVT(2)
+            MOE_CVT(3)
+#undef MOE_CVT
+        }
+        reinterpret_cast<uint2 *>(codes)[u] = bad ? uint2{0, 0} : uint2{c[0], c[1]};
+        scales[u] = (uint8_t)sc;
+    }
+}
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Two products a g rounded once to bf16: the fp32 product rounded first
+// could land on a bf16 middle that it is not on; its error (exact, by fma)
+// then says to which side it belongs.
+__device__ __forceinline__ bool on_middle(float p) { return (__float_as_uint(p) & 0xffffu) == 0x8000u; }
+__device__ __forceinline__ float off_middle(float a, float g) {
     const float p = a * g;
     uint32_t u = __float_as_uint(p);
-    if ((u & 0xffffu) == 0x8000u) {
+    if (on_middle(p)) {
         const float err = fmaf(a, g, -p);
         if (err != 0.f) u += ((err > 0.f) == (p > 0.f)) ? 1 : -1;
     }
-    return f32_to_bf16(__uint_as_float(u));
+    return __uint_as_float(u);
+}
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
 
 template <int FMT, bool VEC, typename DST>
@@ -109,37 +201,47 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t *__r
         const uint32_t c = reinterpret_cast<const uint32_t *>(codes)[u];
         const uint32_t sc = scales[u / kLanes];
         const float s = FMT == MOE_FMT_MXFP4 ? e8m0_f(sc) : e4m3_f(sc);
-        const float g = FMT == MOE_FMT_E2M1 && globals ? globals[by_global((uint64_t)row)] : 1.f;
-        float f[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) f[i] = e2m1_f((c >> (4 * i)) & 15u) * s;   // exact
         DST *o = dst + row * stride + (u - row * upr) * kPer;
-        if constexpr (sizeof(DST) == 4) {
+        f32x2 f[kPer / 2];
+#define MOE_CVT(B) f[B] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, B);
+        MOE_CVT(0)
+        MOE_CVT(1)
+        MOE_CVT(2)
+        MOE_CVT(3)
+#undef MOE_CVT
+        const bool scaled = FMT == MOE_FMT_E2M1 && globals != nullptr;
+        const float g = scaled ? globals[by_global((uint64_t)row)] : 1.f;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) f[i] *= g;
-            if constexpr (VEC) {
-                u32x4 a, b;
+        for (int i = 0; i < kPer / 2; ++i) f[i] = f32x2{f[i].x * s, f[i].y * s};   // exact
+        uint32_t v[sizeof(DST) == 4 ? kPer : kPer / 2];
+        bool middle = false;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = __float_as_uint(f[i]), b[i] = __float_as_uint(f[4 + i]);
-                reinterpret_cast<u32x4 *>(o)[0] = a;
-                reinterpret_cast<u32x4 *>(o)[1] = b;
+        for (int i = 0; i < kPer / 2; ++i) {
+            const f32x2 t = scaled ? f32x2{f[i].x * g, f[i].y * g} : f[i];
+            if constexpr (sizeof(DST) == 4) {
+                v[2 * i] = __float_as_uint(t.x);
+                v[2 * i + 1] = __float_as_uint(t.y);
             } else {
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) o[i] = f[i];
+                v[i] = bf16_pair(t.x, t.y);
+                middle |= on_middle(t.x) | on_middle(t.y);
             }
+        }
+        if constexpr (sizeof(DST) == 2) {
+            if (scaled && middle) {   // one product in 2^16
+#pragma unroll
+                for (int i = 0; i < kPer / 2; ++i) v[i] = bf16_pair(off_middle(f[i].x, g), off_middle(f[i].y, g));
+            }
+        }
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < (int)(sizeof v / 16); ++i)
+                reinterpret_cast<u32x4 *>(o)[i] = u32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+        } else if constexpr (sizeof(DST) == 4) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) o[i] = __uint_as_float(v[i]);
         } else {
-            uint16_t h[kPer];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) h[i] = bf16_once(f[i], g);
-            if constexpr (VEC) {
-                u32x4 a;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = h[2 * i] | ((uint32_t)h[2 * i + 1] << 16);
-                *reinterpret_cast<u32x4 *>(o) = a;
-            } else {
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) o[i] = h[i];
-            }
+            for (int i = 0; i < kPer; ++i) o[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
         }
     }
 }
@@ -155,30 +257,37 @@ int grid_for(int64_t units) {
 hipError_t launch_quantize(int fmt, int type, const RowsParams &p, const void *src, uint8_t *codes,
                            uint8_t *scales, hipStream_t s) {
     if (p.rows == 0) return hipSuccess;
-    const int upr = p.cols / kPer;
-    const int64_t units = p.rows * upr;
     const bool vec = vector_rows(src, p.stride, p.rows, type == MOE_TYPE_F32 ? 4 : 2);
-    const FastDiv by_upr(upr), by_global(p.globals ? p.rows_per_global : 1);
-#define MOE_QUANT(F, V, S)                                                                                \
-    hipLaunchKernelGGL((quantize_kernel<F, V, S>), dim3(grid_for(units)), dim3(kThreads), 0, s,          \
+    const int upr = p.cols / (fmt == MOE_FMT_MXFP4 ? kPer : 2 * kPer);
+    const int64_t units = p.rows * upr;
+    const FastDiv by_upr(upr, units), by_global(p.globals ? p.rows_per_global : 1, p.rows);
+#define MOE_MX(V, S)                                                                                    \
+    hipLaunchKernelGGL((quantize_mx_kernel<V, S>), dim3(grid_for(units)), dim3(kThreads), 0, s,        \
+                       static_cast<const S *>(src), p.stride, units, upr, by_upr, codes, scales)
+#define MOE_E2M1(V, S)                                                                                  \
+    hipLaunchKernelGGL((quantize_e2m1_kernel<V, S>), dim3(grid_for(units)), dim3(kThreads), 0, s,      \
                        static_cast<const S *>(src), p.stride, units, upr, by_upr, p.globals, by_global, \
                        codes, scales)
-#define MOE_QUANT_V(F, S)       \
-    if (vec)                    \
-        MOE_QUANT(F, true, S);  \
-    else                        \
-        MOE_QUANT(F, false, S);
-    if (fmt == MOE_FMT_MXFP4 && type == MOE_TYPE_F32) {
-        MOE_QUANT_V(MOE_FMT_MXFP4, float)
-    } else if (fmt == MOE_FMT_MXFP4) {
-        MOE_QUANT_V(MOE_FMT_MXFP4, uint16_t)
-    } else if (type == MOE_TYPE_F32) {
-        MOE_QUANT_V(MOE_FMT_E2M1, float)
-    } else {
-        MOE_QUANT_V(MOE_FMT_E2M1, uint16_t)
+#define MOE_QUANT(K)            \
+    if (type == MOE_TYPE_F32) { \
+        if (vec)                \
+            K(true, float);     \
+        else                    \
+            K(false, float);    \
+    } else {                    \
+        if (vec)                \
+            K(true, uint16_t);  \
+        else                    \
+            K(false, uint16_t); \
     }
-#undef MOE_QUANT_V
+    if (fmt == MOE_FMT_MXFP4) {
+        MOE_QUANT(MOE_MX)
+    } else {
+        MOE_QUANT(MOE_E2M1)
+    }
 #undef MOE_QUANT
+#undef MOE_E2M1
+#undef MOE_MX
     return hipGetLastError();
 }
 
@@ -188,7 +297,7 @@ hipError_t launch_dequantize(int fmt, int type, const RowsParams &p, const uint8
     const int upr = p.cols / kPer;
     const int64_t units = p.rows * upr;
     const bool vec = vector_rows(dst, p.stride, p.rows, type == MOE_TYPE_F32 ? 4 : 2);
-    const FastDiv by_upr(upr), by_global(p.globals ? p.rows_per_global : 1);
+    const FastDiv by_upr(upr, units), by_global(p.globals ? p.rows_per_global : 1, p.rows);
 #define MOE_DEQ(F, V, S)                                                                              \
     hipLaunchKernelGGL((dequantize_kernel<F, V, S>), dim3(grid_for(units)), dim3(kThreads), 0, s,    \
                        codes, scales, units, upr, by_upr, p.globals, by_global, static_cast<S *>(dst), \

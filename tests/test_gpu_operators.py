@@ -233,6 +233,23 @@ def test_every_bf16_value_and_every_scale(fmt):
     _check_rows(t, fmt)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_e2m1_scales_beside_the_middle_of_two_scales(dtype):
+    # the largest of a block: 6 g times a middle of two E4M3 values, one step of its type either way
+    g = W.rng(12, "scale middles")
+    grid = ref.e4m3_grid()
+    mids = (grid[1:] + grid[:-1]) / 2
+    globs = np.concatenate([[1.0, 0.5, 3.0], (g.random(29) + 0.5) * 2.0 ** g.integers(-30, 30, 29)]).astype(np.float32)
+    step = lambda v, d: torch.nextafter(torch.from_numpy(v).to(dtype), torch.tensor(d, dtype=dtype)).double().numpy()
+    x = np.zeros((len(globs), len(mids) * 3, 16))
+    for i, gl in enumerate(globs):
+        v = torch.from_numpy(6 * np.float64(gl) * mids).to(dtype).double().numpy()
+        x[i, 0::3, 3], x[i, 1::3, 5], x[i, 2::3, 9] = v, -step(v, 0.0), step(v, np.inf)
+        x[i, :, 10] = x[i, :, 3] * 0.3
+    t = torch.from_numpy(x.reshape(len(globs), -1)).to(dtype).cuda()
+    _check_rows(t, "e2m1", torch.from_numpy(globs).cuda(), 1)
+
+
 def test_e2m1_values_beside_the_middle_of_two_codes():
     # every block: largest 6 s g, the rest a middle of two codes times s g, one fp32 step either way
     g = W.rng(13, "middles")
@@ -295,8 +312,12 @@ def test_dequantize_reads_every_code_and_scale():
             s = np.where(sb == 255, np.nan, np.ldexp(1.0, sb - 127))
         else:
             s = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
-        want = (s[:, None] * pair[None, :]).astype(np.float32)
+        with np.errstate(over="ignore"):
+            want = (s[:, None] * pair[None, :]).astype(np.float32)
         assert np.array_equal(out.cpu().numpy(), want, equal_nan=True)
+        half = torch.empty((256, 512), dtype=torch.bfloat16, device="cuda")
+        m.moe_dequantize_rows(FMT[fmt], codes, scales, half)
+        assert np.array_equal(half.float().cpu().numpy(), torch.from_numpy(want).bfloat16().float().numpy(), equal_nan=True)
 
 
 # ---------------------------------------------------------------- products
