@@ -187,6 +187,7 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
 
+// Back: a lane holds 8 MXFP4 codes, or a block of 16 E2M1 ones.
 template <int FMT, bool VEC, typename DST>
 __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t *__restrict__ codes,
                                                               const uint8_t *__restrict__ scales,
@@ -194,42 +195,52 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t *__r
                                                               const float *__restrict__ globals,
                                                               FastDiv by_global, DST *__restrict__ dst,
                                                               int64_t stride) {
-    constexpr int kLanes = FMT == MOE_FMT_MXFP4 ? 4 : 2;
+    constexpr int kWords = FMT == MOE_FMT_MXFP4 ? 1 : 2, kN = 8 * kWords;
     const int64_t step = (int64_t)gridDim.x * kThreads;
     for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units; u += step) {
         const int64_t row = (int64_t)by_upr((uint64_t)u);
-        const uint32_t c = reinterpret_cast<const uint32_t *>(codes)[u];
-        const uint32_t sc = scales[u / kLanes];
+        uint32_t c[kWords];
+        if constexpr (kWords == 2) {
+            const uint2 t = reinterpret_cast<const uint2 *>(codes)[u];
+            c[0] = t.x;
+            c[kWords - 1] = t.y;
+        } else {
+            c[0] = reinterpret_cast<const uint32_t *>(codes)[u];
+        }
+        const uint32_t sc = scales[FMT == MOE_FMT_MXFP4 ? u / 4 : u];
         const float s = FMT == MOE_FMT_MXFP4 ? e8m0_f(sc) : e4m3_f(sc);
-        DST *o = dst + row * stride + (u - row * upr) * kPer;
-        f32x2 f[kPer / 2];
-#define MOE_CVT(B) f[B] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, B);
-        MOE_CVT(0)
-        MOE_CVT(1)
-        MOE_CVT(2)
-        MOE_CVT(3)
+        DST *o = dst + row * stride + (u - row * upr) * kN;
+        f32x2 f[kN / 2];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+#define MOE_CVT(B) f[4 * i + B] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[i], 1.0f, B);
+            MOE_CVT(0)
+            MOE_CVT(1)
+            MOE_CVT(2)
+            MOE_CVT(3)
 #undef MOE_CVT
+        }
         const bool scaled = FMT == MOE_FMT_E2M1 && globals != nullptr;
         const float g = scaled ? globals[by_global((uint64_t)row)] : 1.f;
 #pragma unroll
-        for (int i = 0; i < kPer / 2; ++i) f[i] = f32x2{f[i].x * s, f[i].y * s};   // exact
-        uint32_t v[sizeof(DST) == 4 ? kPer : kPer / 2];
+        for (int i = 0; i < kN / 2; ++i) f[i] = f32x2{f[i].x * s, f[i].y * s};   // exact
+        uint32_t v[sizeof(DST) == 4 ? kN : kN / 2];
         bool middle = false;
 #pragma unroll
-        for (int i = 0; i < kPer / 2; ++i) {
+        for (int i = 0; i < kN / 2; ++i) {
             const f32x2 t = scaled ? f32x2{f[i].x * g, f[i].y * g} : f[i];
             if constexpr (sizeof(DST) == 4) {
                 v[2 * i] = __float_as_uint(t.x);
                 v[2 * i + 1] = __float_as_uint(t.y);
             } else {
                 v[i] = bf16_pair(t.x, t.y);
-                middle |= on_middle(t.x) | on_middle(t.y);
+                if (scaled) middle |= on_middle(t.x) | on_middle(t.y);
             }
         }
         if constexpr (sizeof(DST) == 2) {
-            if (scaled && middle) {   // one product in 2^16
+            if (middle) {   // one product in 2^16
 #pragma unroll
-                for (int i = 0; i < kPer / 2; ++i) v[i] = bf16_pair(off_middle(f[i].x, g), off_middle(f[i].y, g));
+                for (int i = 0; i < kN / 2; ++i) v[i] = bf16_pair(off_middle(f[i].x, g), off_middle(f[i].y, g));
             }
         }
         if constexpr (VEC) {
@@ -238,10 +249,10 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t *__r
                 reinterpret_cast<u32x4 *>(o)[i] = u32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
         } else if constexpr (sizeof(DST) == 4) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) o[i] = __uint_as_float(v[i]);
+            for (int i = 0; i < kN; ++i) o[i] = __uint_as_float(v[i]);
         } else {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) o[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+            for (int i = 0; i < kN; ++i) o[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
         }
     }
 }
@@ -294,7 +305,7 @@ hipError_t launch_quantize(int fmt, int type, const RowsParams &p, const void *s
 hipError_t launch_dequantize(int fmt, int type, const RowsParams &p, const uint8_t *codes,
                              const uint8_t *scales, void *dst, hipStream_t s) {
     if (p.rows == 0) return hipSuccess;
-    const int upr = p.cols / kPer;
+    const int upr = p.cols / (fmt == MOE_FMT_MXFP4 ? kPer : 2 * kPer);
     const int64_t units = p.rows * upr;
     const bool vec = vector_rows(dst, p.stride, p.rows, type == MOE_TYPE_F32 ? 4 : 2);
     const FastDiv by_upr(upr, units), by_global(p.globals ? p.rows_per_global : 1, p.rows);
