@@ -744,10 +744,6 @@ __device__ __forceinline__ u32x4 load_scales(const uint8_t *row, int b0, int nbl
     return v;
 }
 
-// One thread's part of a stage, in registers.
-template <int WLOADS, int XLOADS> struct StagePart {
-    u32x4 w[WLOADS], x[XLOADS];
-};
 template <int N> struct Tiles {
     static constexpr int n = N;
 };
@@ -764,7 +760,7 @@ __global__ __launch_bounds__(kThreads, BT == 256 ? 1 : 2) void mx_tile_kernel(Mx
     constexpr int kWaveRows = kTileRows / kAcross, kWaveRoutes = BT * kAcross / kWaves;
     constexpr int kN = kWaveRows / 32, kT = kWaveRoutes / 32;
     constexpr int kWLoads = kTileRows / 32, kXLoads = BT / 32;
-    constexpr bool kFar = BT < 256;                  // two stages on their way
+    constexpr bool kSkip = BT < 256;                 // route tiles past the run are left out
     __shared__ __align__(16) uint8_t wbuf[2][kTileRows * kStageBytes];
     __shared__ __align__(16) uint8_t xbuf[2][BT * kStageBytes];
     // scales, two stages of all rows at a time: matrix rows, then routes
@@ -843,101 +839,110 @@ __global__ __launch_bounds__(kThreads, BT == 256 ? 1 : 2) void mx_tile_kernel(Mx
         };
 
         const int r0 = wn * kWaveRows + c, t0 = wt * kWaveRoutes + c;
-        // all of k with the wave's first NT route tiles (and, kFar, the
+        // all of k with the wave's first NT route tiles (and, kSkip, the
         // block's first 32 NT routes alone)
         auto all_stages = [&](auto tiles) {
-            constexpr int NT = decltype(tiles)::n, kX = kFar ? NT : kXLoads;
-            using Part = StagePart<kWLoads, kX>;
-            auto fetch = [&](int st, Part &r) {      // stages past the last repeat it
-                st = min(st, stages - 1);
-                const int off = min(st * kStageBlocks + chunk, nblk - 1) * 16;
-#pragma unroll
-                for (int i = 0; i < kWLoads; ++i) r.w[i] = *reinterpret_cast<const u32x4 *>(wp[i] + off);
-#pragma unroll
-                for (int i = 0; i < kX; ++i) r.x[i] = *reinterpret_cast<const u32x4 *>(xp[i] + off);
+            constexpr int NT = decltype(tiles)::n, kX = kSkip ? NT : kXLoads;
+            // what a thread moves in a stage: a part of the next stage from
+            // its register to LDS, and the same part of the stage after that
+            // from memory to the register
+            constexpr int kMoves = kWLoads + kX, kProducts = 4 * kN * NT, kReads = kN + NT;
+            u32x4 part[kMoves];
+            auto from_memory = [&](int i, int st) {      // stages past the last repeat it
+                const int off = min(min(st, stages - 1) * kStageBlocks + chunk, nblk - 1) * 16;
+                part[i] = *reinterpret_cast<const u32x4 *>((i < kWLoads ? wp[i < kWLoads ? i : 0]
+                                                                        : xp[i < kWLoads ? 0 : i - kWLoads]) + off);
             };
-            auto put = [&](int b, const Part &r) {
-#pragma unroll
-                for (int i = 0; i < kWLoads; ++i)
-                    *reinterpret_cast<u32x4 *>(&wbuf[b][i * 4096 + tid * 16]) = r.w[i];
-#pragma unroll
-                for (int i = 0; i < kX; ++i) *reinterpret_cast<u32x4 *>(&xbuf[b][i * 4096 + tid * 16]) = r.x[i];
+            auto to_lds = [&](int i, int b) {
+                uint8_t *to = i < kWLoads ? &wbuf[b][i * 4096] : &xbuf[b][(i - kWLoads) * 4096];
+                *reinterpret_cast<u32x4 *>(to + tid * 16) = part[i];
             };
-            // stage st, from buffer B = st & 1; `next` (the stage after) goes
-            // to the other buffer, which nobody has read since the last
-            // barrier, and so do the next two stages' scales in every second
-            auto stage = [&](int b, int st, const Part &next) {
+            // Stage st from buffer b = st & 1, into which the stage after next
+            // goes once all have read it; the next goes to the other buffer,
+            // the scales of the next two stages in every second stage.
+            //
+            // A wave issues in order, and a request to memory can hold it up
+            // for a hundred cycles, an LDS access for tens.  So the moves and
+            // the operand reads of the next step are set between the matrix
+            // instructions, of 32 cycles each, one or two at a time, and kept
+            // there (sched_barrier): with all requests before the products a
+            // stage of BT 256 took 6100 cycles, 2050 of them products.
+            auto stage = [&](int b, int st) {
                 const int g = (st >> 1) & 1;
                 uint32_t sa[kN], sb[NT];
-#pragma unroll
-                for (int i = 0; i < kN; ++i)
-                    sa[i] = *reinterpret_cast<const uint32_t *>(&sc[g][r0 + 32 * i][kStageBlocks * b + 4 * h]);
+                u32x4 wa[2][kN], xb[2][NT];
+                auto read = [&](int e, int s) {          // operand e of step s
+                    const int slot = ((4 * h + s) ^ (c & 7)) * 16;
+                    if (e < NT)
+                        xb[s & 1][e < NT ? e : 0] =
+                            *reinterpret_cast<const u32x4 *>(&xbuf[b][(t0 + 32 * e) * kStageBytes + slot]);
+                    else
+                        wa[s & 1][e < NT ? 0 : e - NT] =
+                            *reinterpret_cast<const u32x4 *>(&wbuf[b][(r0 + 32 * (e - NT)) * kStageBytes + slot]);
+                };
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
                     sb[i] = *reinterpret_cast<const uint32_t *>(
                         &sc[g][kTileRows + t0 + 32 * i][kStageBlocks * b + 4 * h]);
-#define MOE_READ(S)                                                                                       \
-    u32x4 wa##S[kN], xb##S[NT];                                                                           \
-    {                                                                                                     \
-        const int slot = ((4 * h + S) ^ (c & 7)) * 16;                                                    \
-        _Pragma("unroll") for (int i = 0; i < NT; ++i) xb##S[i] =                                         \
-            *reinterpret_cast<const u32x4 *>(&xbuf[b][(t0 + 32 * i) * kStageBytes + slot]);               \
-        _Pragma("unroll") for (int i = 0; i < kN; ++i) wa##S[i] =                                         \
-            *reinterpret_cast<const u32x4 *>(&wbuf[b][(r0 + 32 * i) * kStageBytes + slot]);               \
+#pragma unroll
+                for (int i = 0; i < kN; ++i)
+                    sa[i] = *reinterpret_cast<const uint32_t *>(&sc[g][r0 + 32 * i][kStageBlocks * b + 4 * h]);
+#pragma unroll
+                for (int e = 0; e < kReads; ++e) read(e, 0);
+#define MOE_STEP(S)                                                                                              \
+    _Pragma("unroll") for (int m = 0; m < kN * NT; ++m) {                                                        \
+        const int i = m / NT, j = m % NT, at = S * kN * NT + m;                                                  \
+        __builtin_amdgcn_sched_barrier(0);                                                                       \
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(wa[S & 1][i]), widen(xb[S & 1][j]),   \
+                                                                    acc[i][j], kFp4, kFp4, S, (int)sa[i], S,    \
+                                                                    (int)sb[j]);                                 \
+        if (S < 3) {                                                                                             \
+            _Pragma("unroll") for (int e = 0; e < kReads; ++e)                                                   \
+                if (e * kN * NT / kReads == m) read(e, S + 1);                                                   \
+        }                                                                                                        \
+        _Pragma("unroll") for (int t = 0; t < kMoves; ++t)                                                       \
+            if (t * kProducts / kMoves == at) {                                                                  \
+                to_lds(t, b ^ 1);                                                                                \
+                from_memory(t, st + 2);                                                                          \
+            }                                                                                                    \
+        if ((!kSkip || b == 1) && at == kProducts - 1) {                                                         \
+            scales_put(g ^ 1);                                                                                   \
+            scales_fetch(((st + 1) >> 1) + 1);                                                                   \
+        }                                                                                                        \
     }
-#define MOE_MULTIPLY(S)                                                                                   \
-    _Pragma("unroll") for (int i = 0; i < kN; ++i) _Pragma("unroll") for (int j = 0; j < NT; ++j)         \
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                                      \
-            widen(wa##S[i]), widen(xb##S[j]), acc[i][j], kFp4, kFp4, S, (int)sa[i], S, (int)sb[j]);
-                MOE_READ(0)
-                MOE_READ(1)
-                MOE_MULTIPLY(0)
-                MOE_READ(2)
-                MOE_MULTIPLY(1)
-                MOE_READ(3)
-                MOE_MULTIPLY(2)
+                MOE_STEP(0)
+                MOE_STEP(1)
+                MOE_STEP(2)
+                MOE_STEP(3)
+#undef MOE_STEP
                 __builtin_amdgcn_sched_barrier(0);
-                put(b ^ 1, next);
-                if (!kFar || b == 1) scales_put(g ^ 1);
-                __builtin_amdgcn_sched_barrier(0);
-                MOE_MULTIPLY(3)
-#undef MOE_READ
-#undef MOE_MULTIPLY
                 lds_barrier();
             };
 
             scales_fetch(0);
-            if constexpr (kFar) {
-                Part even, odd;
-                fetch(0, even);
-                fetch(1, odd);
-                scales_put(0);
-                put(0, even);
-                lds_barrier();
+#pragma unroll
+            for (int i = 0; i < kMoves; ++i) from_memory(i, 0);
+            scales_put(0);
+#pragma unroll
+            for (int i = 0; i < kMoves; ++i) to_lds(i, 0);
+            scales_fetch(1);
+#pragma unroll
+            for (int i = 0; i < kMoves; ++i) from_memory(i, 1);
+            lds_barrier();
+            if constexpr (kSkip) {
                 for (int st = 0; st < stages; st += 2) {
-                    scales_fetch((st >> 1) + 1);
-                    fetch(st + 2, even);
-                    stage(0, st, odd);
+                    stage(0, st);
                     if (st + 1 >= stages) break;
-                    fetch(st + 3, odd);
-                    stage(1, st + 1, even);
+                    stage(1, st + 1);
                 }
             } else {
                 // (two copies of the stage would not fit the registers: the
-                // scales are fetched and put again in the second)
-                Part next;
-                fetch(0, next);
-                scales_put(0);
-                put(0, next);
-                lds_barrier();
-                for (int st = 0; st < stages; ++st) {
-                    scales_fetch((st >> 1) + 1);
-                    fetch(st + 1, next);
-                    stage(st & 1, st, next);
-                }
+                // scales are put and fetched again in the second)
+#pragma unroll 1
+                for (int st = 0; st < stages; ++st) stage(st & 1, st);
             }
         };
-        if constexpr (kFar) {
+        if constexpr (kSkip) {
             static_assert(kT <= 4, "route tiles of a wave");
             if (live > 96)
                 all_stages(Tiles<kT>{});

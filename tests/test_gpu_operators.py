@@ -78,6 +78,10 @@ def _check_route(logits, K, bias=None, **kw):
     (300, 33, 2, dict(score="softmax", groups=11, top_groups=11)),
     (600, 160, 2, dict(score="softmax")),
     (1500, 48, 4, dict(score="sigmoid", groups=4, top_groups=2, bias=True)),
+    (4097, 48, 4, dict(score="sigmoid", groups=4, top_groups=2, bias=True)),
+    (4098, 130, 12, dict(score="softmax", bias=True)),
+    (4099, 20, 12, dict(score="softmax", renorm=False)),
+    (4100, 200, 13, dict(score="sigmoid")),
 ])
 def test_route_matches_the_plain_form(T, E, K, kw, dtype):
     _say("route", T, E, K, kw, dtype)
@@ -135,6 +139,27 @@ def test_route_orders_scores_closer_than_an_fp32_rounding():
     _check_route(torch.full((3, E), 0.75, device="cuda"), K, bias=bias, score="sigmoid")
     _check_route(torch.full((3, E), 0.75, device="cuda"), K, bias=bias, score="sigmoid", groups=8, top_groups=3,
                  top2=True)
+
+
+@pytest.mark.parametrize("score,groups,top2,with_bias", [("sigmoid", 1, False, True), ("softmax", 1, False, False),
+                                                         ("sigmoid", 8, True, True), ("softmax", 8, False, True)])
+def test_many_rows_of_every_kind_side_by_side(score, groups, top2, with_bias):
+    # four rows to a wave: rows with few candidates next to rows that are finished by themselves
+    T, E, K = 4102, 192, 6
+    g = W.rng(5, "many", score, groups)
+    x = g.standard_normal((T, E)).astype(np.float32)
+    x[1::7] = -np.inf
+    x[2::7] = 0.5                                             # all equal
+    x[3::7, 5:] = -np.inf                                     # fewer than K
+    x[4::11] = np.round(x[4::11])                             # many equal
+    x[5::11, :100] = np.finfo(np.float32).min
+    x[6::13] = np.nan
+    x[8::13, 20] = np.inf
+    x[9::17] *= 1e-7
+    bias = torch.from_numpy((g.standard_normal(E) * 0.05).astype(np.float32)).cuda() if with_bias else None
+    for renorm in (True, False):
+        _check_route(torch.from_numpy(x).cuda(), K, bias=bias, score=score, groups=groups,
+                     top_groups=min(3, groups), top2=top2, renorm=renorm)
 
 
 @pytest.mark.parametrize("E,groups,top_groups,top2", [(64, 1, 1, False), (256, 1, 1, False), (256, 8, 3, True),
