@@ -42,6 +42,13 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb
 
 __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
 
+// Two fp32 rounded to bf16, by the hardware's conversion (to nearest, ties to even).
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+
 // Four consecutive outputs col .. col + 3 of a row of cols; `whole`: rows
 // start on whole vectors of four and cols is a multiple of 4.
 __device__ __forceinline__ void store4(float *o, int col, int cols, bool whole, f32x4 v) {
@@ -56,9 +63,7 @@ __device__ __forceinline__ void store4(float *o, int col, int cols, bool whole, 
 __device__ __forceinline__ void store4(uint16_t *o, int col, int cols, bool whole, f32x4 v) {
     if (whole) {
         if (col < cols)
-            *reinterpret_cast<uint2 *>(o + col) =
-                uint2{f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16),
-                      f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16)};
+            *reinterpret_cast<uint2 *>(o + col) = uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -369,7 +374,6 @@ template <int U, bool VEC> struct StepScales {
     __device__ __forceinline__ uint32_t at(int u, int q) const { return VEC ? v[u] >> (8 * q) : v[u]; }
 };
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 // 32 bf16 as an MX block: codes and scale byte (0xFF and zeros where one of
@@ -706,8 +710,8 @@ __global__ __launch_bounds__(kThreads, 3) void mx_stream_kernel(MxParams p, int 
 // lane holds rows 8 (i / 4) + 4 h + i % 4, i = 0..15, of column (route) c.
 //
 // An LDS row is the stage's 128 bytes of one operand row, eight 16-byte
-// chunks (one MX block each); chunk j lies in slot j ^ (row & 7), which
-// spreads the rows of an operand read over all banks.
+// chunks (one MX block each); chunk j lies in slot j ^ (row / 2 % 8): two rows
+// fill the 64 banks, and the 16 rows that are read at once hit each bank once.
 constexpr int kStageBlocks = 8, kStageBytes = 16 * kStageBlocks;
 // Rows of the matrix a block takes: at BT 256 as many as the registers hold
 // (two thirds of the device's rate need 128 rows for an operand byte); below,
@@ -754,34 +758,43 @@ __global__ __launch_bounds__(kThreads, BT == 256 ? 1 : 2) void mx_tile_kernel(Mx
                                                               const int32_t *__restrict__ n_runs,
                                                               const Run *__restrict__ runs,
                                                               const int32_t *__restrict__ routes, int R,
-                                                              int row_tiles, OUT *__restrict__ out) {
+                                                              int max_runs, int row_tiles, FastDiv by_K,
+                                                              OUT *__restrict__ out) {
     constexpr int kTileRows = tile_rows(BT);
     constexpr int kAcross = BT == 256 ? 2 : 4;       // waves along the rows; the others along the routes
     constexpr int kWaveRows = kTileRows / kAcross, kWaveRoutes = BT * kAcross / kWaves;
     constexpr int kN = kWaveRows / 32, kT = kWaveRoutes / 32;
     constexpr int kWLoads = kTileRows / 32, kXLoads = BT / 32;
     constexpr bool kSkip = BT < 256;                 // route tiles past the run are left out
-    __shared__ __align__(16) uint8_t wbuf[2][kTileRows * kStageBytes];
-    __shared__ __align__(16) uint8_t xbuf[2][BT * kStageBytes];
-    // scales, two stages of all rows at a time: matrix rows, then routes
+    // scales are kept two stages of all rows at a time: matrix rows, then routes
     constexpr int kSLoads = (kTileRows + BT + kThreads - 1) / kThreads;
-    __shared__ __align__(16) uint8_t sc[2][kSLoads * kThreads][2 * kStageBlocks];
+    struct Stages {
+        uint8_t w[2][kTileRows * kStageBytes], x[2][BT * kStageBytes];
+        uint8_t sc[2][kSLoads * kThreads][2 * kStageBlocks];
+    };
+    __shared__ __align__(16) uint8_t lds[sizeof(Stages)];
+    Stages &buf = *reinterpret_cast<Stages *>(lds);
+    auto &wbuf = buf.w;
+    auto &xbuf = buf.x;
+    auto &sc = buf.sc;
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     const int c = lane & 31, h = lane / 32;
-    // Consecutive workgroups go to the eight XCDs in turn; each XCD takes a
-    // contiguous part of (run, row tile), so its L2 sees the runs of one
-    // matrix and the row tiles of one run together.
-    const int total = (n_runs != nullptr ? n_runs[0] : (R + BT - 1) / BT) * row_tiles;
-    const int per = (total + 7) / 8;
-    const int item = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
-    if ((int)(blockIdx.x / 8) >= per || item >= total) return;
-    const int ri = item / row_tiles, tile = item - ri * row_tiles;
+    // Consecutive workgroups go to the eight XCDs in turn: a run's row tiles
+    // go to one of them, one behind the other, so that its L2 holds their
+    // routes' x.  (The run is read beside the number of runs; past it there
+    // is room in the table, but nothing that is used.)
+    const int ri = (int)(blockIdx.x / 8) / row_tiles * 8 + (int)(blockIdx.x % 8);
+    const int tile = (int)(blockIdx.x / 8) % row_tiles;
+    if (ri >= max_runs) return;
     Run run;
-    if (n_runs != nullptr)
+    if (n_runs != nullptr) {
+        const int n = n_runs[0];
         run = runs[ri];
-    else
+        if (ri >= n) return;
+    } else {
         run = Run{0, ri * BT, min(BT, R - ri * BT), 0};
+    }
 
     const int cols = SWIGLU ? p.n / 2 : p.n;
     constexpr int kCols = SWIGLU ? kTileRows / 2 : kTileRows;   // output columns of the block
@@ -816,17 +829,17 @@ __global__ __launch_bounds__(kThreads, BT == 256 ? 1 : 2) void mx_tile_kernel(Mx
 
     if (run.row >= 0) {
         const uint8_t *wp[kWLoads], *xp[kXLoads];
-        const int lr = tid / 8, chunk = (tid & 7) ^ (lr & 7);
+        const int lr = tid / 8, chunk = (tid & 7) ^ ((lr >> 1) & 7);
 #pragma unroll
         for (int i = 0; i < kWLoads; ++i) wp[i] = p.codes + matrix_row(32 * i + lr) * row_bytes;
 #pragma unroll
-        for (int i = 0; i < kXLoads; ++i) xp[i] = xc + (int64_t)(route_at(32 * i + lr) / p.K) * row_bytes;
+        for (int i = 0; i < kXLoads; ++i) xp[i] = xc + (int64_t)by_K(route_at(32 * i + lr)) * row_bytes;
         const uint8_t *sp[kSLoads];
 #pragma unroll
         for (int i = 0; i < kSLoads; ++i) {
             const int r = tid + i * kThreads;
             sp[i] = r < kTileRows ? p.scales + matrix_row(r) * nblk
-                                  : xs + (int64_t)(route_at(min(r - kTileRows, BT - 1)) / p.K) * nblk;
+                                  : xs + (int64_t)by_K(route_at(min(r - kTileRows, BT - 1))) * nblk;
         }
         u32x4 sr[kSLoads];
         auto scales_fetch = [&](int g) {
@@ -872,7 +885,7 @@ __global__ __launch_bounds__(kThreads, BT == 256 ? 1 : 2) void mx_tile_kernel(Mx
                 uint32_t sa[kN], sb[NT];
                 u32x4 wa[2][kN], xb[2][NT];
                 auto read = [&](int e, int s) {          // operand e of step s
-                    const int slot = ((4 * h + s) ^ (c & 7)) * 16;
+                    const int slot = ((4 * h + s) ^ ((c >> 1) & 7)) * 16;
                     if (e < NT)
                         xb[s & 1][e < NT ? e : 0] =
                             *reinterpret_cast<const u32x4 *>(&xbuf[b][(t0 + 32 * e) * kStageBytes + slot]);
@@ -957,28 +970,61 @@ __global__ __launch_bounds__(kThreads, BT == 256 ? 1 : 2) void mx_tile_kernel(Mx
         }
     }
 
-    // lane (c, h) holds rows 8 g + 4 h .. + 3 (g = 0..3) of its row tiles for route c
-    const bool whole = cols % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (4 * sizeof(OUT) - 1)) == 0;
+    // The results go through LDS (the stages are done with it), so that whole
+    // rows are written: lane (c, h) holds four columns each of 64 places, of
+    // a route of its own.  Written from the registers they took a third of
+    // the kernel's time at BT 256.  fp32 results of BT 256 go in two halves.
+    constexpr int kPitch = kCols * (int)sizeof(OUT) + 16;
+    constexpr int kPasses = BT * kPitch <= (int)sizeof(Stages) ? 1 : kWaves / kAcross;
+    constexpr int kPassRoutes = BT / kPasses;
+    static_assert(kPassRoutes * kPitch <= (int)sizeof(Stages) && (kPasses == 1 || kPassRoutes == kWaveRoutes), "LDS");
+    constexpr int kUnits = kCols * (int)sizeof(OUT) / 16, kPerUnit = 16 / (int)sizeof(OUT);
+    const bool whole = cols % kPerUnit == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
 #pragma unroll
-    for (int j = 0; j < kT; ++j) {
-        const int at = wt * kWaveRoutes + 32 * j + c;
-        if (at >= run.count) continue;
-        OUT *o = out + (int64_t)route_at(at) * cols;
-        // groups of four rows: 4 kN of them, with SwiGLU the first half gate, the second up
-        constexpr int kGroups = SWIGLU ? 2 * kN : 4 * kN;
+    for (int pass = 0; pass < kPasses; ++pass) {
+        if (pass > 0) lds_barrier();             // the first half has been read
+        if (kPasses == 1 || wt == pass) {
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-            const int col = j0 + wn * (kCols / kAcross) + 8 * g + 4 * h;
-            f32x4 v;
+            for (int j = 0; j < kT; ++j) {
+                const int at = (kPasses == 1 ? wt * kWaveRoutes : 0) + 32 * j + c;
+                // groups of four rows: 4 kN of them, with SwiGLU the first half gate, the second up
+                constexpr int kGroups = SWIGLU ? 2 * kN : 4 * kN;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] = acc[g / 4][j][4 * (g % 4) + e];
-                if constexpr (SWIGLU) {
-                    constexpr int kUp = 2 * kN;
-                    v[e] = silu(v[e]) * acc[(g + kUp) / 4][j][4 * ((g + kUp) % 4) + e];
+                for (int g = 0; g < kGroups; ++g) {
+                    const int col = wn * (kCols / kAcross) + 8 * g + 4 * h;
+                    f32x4 v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = acc[g / 4][j][4 * (g % 4) + e];
+                        if constexpr (SWIGLU) {
+                            constexpr int kUp = 2 * kN;
+                            v[e] = silu(v[e]) * acc[(g + kUp) / 4][j][4 * ((g + kUp) % 4) + e];
+                        }
+                    }
+                    uint8_t *to = lds + at * kPitch + col * (int)sizeof(OUT);
+                    if constexpr (sizeof(OUT) == 4)
+                        *reinterpret_cast<f32x4 *>(to) = v;
+                    else
+                        *reinterpret_cast<uint2 *>(to) = uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
                 }
             }
-            store4(o, col, cols, whole, v);
+        }
+        lds_barrier();
+        const int n = min(run.count - pass * kPassRoutes, kPassRoutes);
+        if (whole) {
+            for (int i = tid; i < n * kUnits; i += kThreads) {
+                const int t = i / kUnits, col = i % kUnits * kPerUnit;
+                if (j0 + col >= cols) continue;
+                *reinterpret_cast<u32x4 *>(out + (int64_t)route_at(pass * kPassRoutes + t) * cols + j0 + col) =
+                    *reinterpret_cast<const u32x4 *>(lds + t * kPitch + col * (int)sizeof(OUT));
+            }
+        } else {
+            for (int i = tid; i < n * kCols; i += kThreads) {
+                const int t = i / kCols, col = i % kCols;
+                if (j0 + col >= cols) continue;
+                out[(int64_t)route_at(pass * kPassRoutes + t) * cols + j0 + col] =
+                    *reinterpret_cast<const OUT *>(lds + t * kPitch + col * (int)sizeof(OUT));
+            }
         }
     }
 }
@@ -1048,11 +1094,12 @@ hipError_t launch_tile(const MxParams &p, const uint8_t *xc, const uint8_t *xs, 
                        const Run *runs, const int32_t *routes, int R, int64_t max_runs, hipStream_t s) {
     const int per = p.swiglu ? tile_rows(BT) / 2 : tile_rows(BT), cols = p.swiglu ? p.n / 2 : p.n;
     const int row_tiles = (cols + per - 1) / per;
-    const unsigned grid = (unsigned)((max_runs * row_tiles + 7) / 8 * 8);
+    const unsigned grid = (unsigned)((max_runs + 7) / 8 * 8 * row_tiles);
+    const FastDiv by_K(p.K, (uint64_t)R);
     const uintptr_t sp = reinterpret_cast<uintptr_t>(p.scales);
 #define MOE_TILE(S, V)                                                                                          \
     hipLaunchKernelGGL((mx_tile_kernel<BT, S, V, OUT>), dim3(grid), dim3(kThreads), 0, s, p, xc, xs, n_runs, runs, \
-                       routes, R, row_tiles, static_cast<OUT *>(p.out))
+                       routes, R, (int)max_runs, row_tiles, by_K, static_cast<OUT *>(p.out))
 #define MOE_TILE_S(S)                        \
     if (p.k % 512 == 0 && sp % 16 == 0)      \
         MOE_TILE(S, 16);                     \
