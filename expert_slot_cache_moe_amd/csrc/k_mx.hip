@@ -812,10 +812,13 @@ __global__ __launch_bounds__(kThreads, BT == 256 ? 1 : 2) void mx_tile_kernel(Mx
             return (int64_t)run.row * p.n + min(j0 + r, cols - 1);
         }
     };
-    auto route_at = [&](int i) {
-        const int at = run.start + min(i, run.count - 1);
-        return n_runs != nullptr ? routes[at] : at;
-    };
+    // the run's routes, the last repeated past its end
+    __shared__ int32_t list[BT];
+    if (tid < BT) {
+        const int at = run.start + min(tid, run.count - 1);
+        list[tid] = n_runs != nullptr ? routes[at] : at;
+    }
+    lds_barrier();
 
     const int wn = wave % kAcross, wt = wave / kAcross;
     const int live = run.count - wt * kWaveRoutes;   // the wave's routes in the run
@@ -833,13 +836,13 @@ __global__ __launch_bounds__(kThreads, BT == 256 ? 1 : 2) void mx_tile_kernel(Mx
 #pragma unroll
         for (int i = 0; i < kWLoads; ++i) wp[i] = p.codes + matrix_row(32 * i + lr) * row_bytes;
 #pragma unroll
-        for (int i = 0; i < kXLoads; ++i) xp[i] = xc + (int64_t)by_K(route_at(32 * i + lr)) * row_bytes;
+        for (int i = 0; i < kXLoads; ++i) xp[i] = xc + (int64_t)by_K(list[32 * i + lr]) * row_bytes;
         const uint8_t *sp[kSLoads];
 #pragma unroll
         for (int i = 0; i < kSLoads; ++i) {
             const int r = tid + i * kThreads;
             sp[i] = r < kTileRows ? p.scales + matrix_row(r) * nblk
-                                  : xs + (int64_t)by_K(route_at(min(r - kTileRows, BT - 1))) * nblk;
+                                  : xs + (int64_t)by_K(list[min(r - kTileRows, BT - 1)]) * nblk;
         }
         u32x4 sr[kSLoads];
         auto scales_fetch = [&](int g) {
@@ -1015,14 +1018,14 @@ __global__ __launch_bounds__(kThreads, BT == 256 ? 1 : 2) void mx_tile_kernel(Mx
             for (int i = tid; i < n * kUnits; i += kThreads) {
                 const int t = i / kUnits, col = i % kUnits * kPerUnit;
                 if (j0 + col >= cols) continue;
-                *reinterpret_cast<u32x4 *>(out + (int64_t)route_at(pass * kPassRoutes + t) * cols + j0 + col) =
+                *reinterpret_cast<u32x4 *>(out + (int64_t)list[pass * kPassRoutes + t] * cols + j0 + col) =
                     *reinterpret_cast<const u32x4 *>(lds + t * kPitch + col * (int)sizeof(OUT));
             }
         } else {
             for (int i = tid; i < n * kCols; i += kThreads) {
                 const int t = i / kCols, col = i % kCols;
                 if (j0 + col >= cols) continue;
-                out[(int64_t)route_at(pass * kPassRoutes + t) * cols + j0 + col] =
+                out[(int64_t)list[pass * kPassRoutes + t] * cols + j0 + col] =
                     *reinterpret_cast<const OUT *>(lds + t * kPitch + col * (int)sizeof(OUT));
             }
         }
