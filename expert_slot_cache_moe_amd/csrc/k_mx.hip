@@ -232,7 +232,7 @@ constexpr int kWaves = 4, kThreads = kWaves * kWave;
 // needed, so that no launch of its own has to do that first.
 //
 // Lists of routes come in three ways:
-//   kRuns    from mx_group_kernel (or, without ids, consecutive rows);
+//   kRuns    from mx_prepare_kernel (or, without ids, consecutive rows);
 //   kByRoute slot r is route r: the first route of its matrix row takes all
 //            of that row's routes, the others leave;
 //   kByRow   slot i is matrix row i, slot P the routes without a row.
@@ -320,18 +320,26 @@ __device__ __forceinline__ bool run_list(RouteList &l, int slot, int run_length,
     return true;
 }
 
-// Zeros in columns [j0, j0 + width) of every route of a list, by THREADS threads.
+// Zeros in columns [j0, j0 + width) of every route of a list, by THREADS
+// threads, 16 bytes at a time where rows are whole vectors (j0 and the
+// unclipped width always are).
 template <int THREADS>
 __device__ __forceinline__ void zero_rows(const MxParams &p, const RouteList &l, int cols, int j0, int width, int tid) {
-    width = min(width, cols - j0);
-    if (width <= 0) return;
-    for (int i = tid; i < l.count * width; i += THREADS) {
-        const int t = i / width;
-        const int64_t o = (int64_t)l.route(t) * cols + j0 + (i - t * width);
-        if (p.out_type == MOE_TYPE_F32)
-            static_cast<float *>(p.out)[o] = 0.f;
+    const int size = p.out_type == MOE_TYPE_F32 ? 4 : 2;
+    const int64_t row_bytes = (int64_t)cols * size;
+    const bool whole = row_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
+    const int unit = whole ? 16 : size, units = min(width, cols - j0) * size / unit;
+    if (units <= 0) return;
+    uint8_t *out = static_cast<uint8_t *>(p.out) + (int64_t)j0 * size;
+    for (int i = tid; i < l.count * units; i += THREADS) {
+        const int t = i / units;
+        uint8_t *o = out + l.route(t) * row_bytes + (int64_t)(i - t * units) * unit;
+        if (whole)
+            *reinterpret_cast<u32x4 *>(o) = u32x4{0u, 0u, 0u, 0u};
+        else if (size == 4)
+            *reinterpret_cast<uint32_t *>(o) = 0u;
         else
-            static_cast<uint16_t *>(p.out)[o] = 0;
+            *reinterpret_cast<uint16_t *>(o) = 0;
     }
 }
 
@@ -446,13 +454,13 @@ template <int U, bool VEC, int kM> struct MatrixChunk {
 // SwiGLU 16 gate and 16 up rows) and split k, every fourth chunk of U steps
 // each; their sums are added in LDS, in wave order.  A lane's part of x for
 // one step is one whole MX block of one token, quantised in registers.
-template <bool SWIGLU, int U, bool VEC, int NT, bool INLINE>
+template <bool SWIGLU, int U, bool VEC, bool INLINE>
 __global__ __launch_bounds__(kThreads) void mx_split_kernel(MxParams p, int mode, bool x_vec,
                                                             const int32_t *__restrict__ n_runs,
                                                             const Run *__restrict__ runs,
                                                             const int32_t *__restrict__ routes, int R) {
     constexpr int kM = SWIGLU ? 2 : 1;
-    __shared__ f32x4 part[kWaves][kM][NT][kWave];
+    __shared__ f32x4 part[kWaves][kM][kWave];
     __shared__ ListLds lds;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     const int c = lane & (kTile - 1), q = lane / kTile;
@@ -483,7 +491,7 @@ __global__ __launch_bounds__(kThreads) void mx_split_kernel(MxParams p, int mode
         l.at = lds.routes;
         if (l.count == 0 || (mode == kByRoute && lds.routes[0] < (int)blockIdx.y)) return;
     } else {
-        if (!run_list(l, blockIdx.y, kTile * NT, n_runs, runs, routes, R)) return;
+        if (!run_list(l, blockIdx.y, kTile, n_runs, runs, routes, R)) return;
         request(l.row);
     }
     if (l.row < 0) {
@@ -493,59 +501,40 @@ __global__ __launch_bounds__(kThreads) void mx_split_kernel(MxParams p, int mode
     const bool f32_out = p.out_type == MOE_TYPE_F32;
     const bool whole = cols % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & (f32_out ? 15 : 7)) == 0;
 
-    for (int base = 0; base < l.count; base += kTile * NT) {
-        f32x4 acc[kM][NT];
+    for (int base = 0; base < l.count; base += kTile) {
+        f32x4 acc[kM];
 #pragma unroll
-        for (int m = 0; m < kM; ++m)
+        for (int m = 0; m < kM; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const int route = l.route(min(base + c, l.count - 1));
+        const uint16_t *xr = p.x + (int64_t)(route / p.K) * p.x_stride;
+        for (int s0 = wave * U; s0 < steps; s0 += kWaves * U) {
+            // the first pass's first chunk is there already
+            if (base > 0 || s0 != wave * U) w.load(ax, as, s0, nblk, q);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        int route[NT];
-        const uint16_t *xr[NT];
+            for (int u = 0; u < U; ++u) {
+                const int b = 4 * (s0 + u) + q;
+                u32x4 xv[4];
+                load_block(xr + 32 * (VEC ? b : min(b, nblk - 1)), x_vec, xv);
+                uint32_t sb;
+                const u32x4 bv = quantize_block(xv, sb);
+                if (!VEC && b >= nblk) sb = 0u;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            route[t] = l.route(min(base + t * kTile + c, l.count - 1));
-            xr[t] = p.x + (int64_t)(route[t] / p.K) * p.x_stride;
-        }
-        {
-            for (int s0 = wave * U; s0 < steps; s0 += kWaves * U) {
-                // the first pass's first chunk is there already
-                if (base > 0 || s0 != wave * U) w.load(ax, as, s0, nblk, q);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if (t > 0 && base + t * kTile >= l.count) break;
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int b = 4 * (s0 + u) + q;
-                        u32x4 xv[4];
-                        load_block(xr[t] + 32 * (VEC ? b : min(b, nblk - 1)), x_vec, xv);
-                        uint32_t sb;
-                        const u32x4 bv = quantize_block(xv, sb);
-                        if (!VEC && b >= nblk) sb = 0u;
-#pragma unroll
-                        for (int m = 0; m < kM; ++m) acc[m][t] = mfma(w.a[m][u], w.s[m].at(u, q), bv, sb, acc[m][t]);
-                    }
-                }
+                for (int m = 0; m < kM; ++m) acc[m] = mfma(w.a[m][u], w.s[m].at(u, q), bv, sb, acc[m]);
             }
         }
         if (base > 0) lds_barrier();         // the last pass has read its sums
 #pragma unroll
-        for (int m = 0; m < kM; ++m)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) part[wave][m][t][lane] = acc[m][t];
+        for (int m = 0; m < kM; ++m) part[wave][m][lane] = acc[m];
         lds_barrier();
-        // wave t adds and stores the pass's tile t
+        if (wave != 0 || base + c >= l.count) continue;
+        f32x4 v[kM];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if (wave != t || base + t * kTile + c >= l.count) continue;
-            f32x4 v[kM];
+        for (int m = 0; m < kM; ++m) {
+            v[m] = part[0][m][lane];
 #pragma unroll
-            for (int m = 0; m < kM; ++m) {
-                v[m] = part[0][m][t][lane];
-#pragma unroll
-                for (int o = 1; o < kWaves; ++o) v[m] += part[o][m][t][lane];
-            }
-            store_columns<SWIGLU>(p, f32_out, route[t], cols, j0 + 4 * q, whole, v);
+            for (int o = 1; o < kWaves; ++o) v[m] += part[o][m][lane];
         }
+        store_columns<SWIGLU>(p, f32_out, route, cols, j0 + 4 * q, whole, v);
     }
 }
 
@@ -561,12 +550,12 @@ __global__ __launch_bounds__(kThreads) void mx_split_kernel(MxParams p, int mode
 // serve every pass over a long list.
 constexpr int kSpanBlocks = 64;
 
-template <bool SWIGLU, int U, bool VEC, bool INLINE>
+template <bool SWIGLU, bool VEC, bool INLINE>
 __global__ __launch_bounds__(kThreads, 3) void mx_stream_kernel(MxParams p, int mode, bool x_vec, int slots,
                                                              int pass_blocks, const int32_t *__restrict__ n_runs,
                                                              const Run *__restrict__ runs,
                                                              const int32_t *__restrict__ routes, int R) {
-    constexpr int kM = 2;
+    constexpr int kM = 2, U = 2;
     constexpr int kCols = SWIGLU ? kTile : 2 * kTile;       // output columns of a wave
     __shared__ __align__(16) u32x4 xc[kSpanBlocks][kTile];
     __shared__ uint8_t xs[kSpanBlocks][kTile];
@@ -1057,20 +1046,18 @@ hipError_t launch_stream_shape(const MxParams &p, int mode, const int32_t *n_run
     const int wide = (cols + block_cols - 1) / block_cols, passes = mode == kByRow ? kPassBlocks : 1;
     if (wide * slots >= kManyBlocks) {
         const dim3 grid((unsigned)(wide * slots * passes));
-#define MOE_STREAM(U, VEC)                                                                                     \
-    hipLaunchKernelGGL((mx_stream_kernel<SWIGLU, U, VEC, INLINE>), grid, dim3(kThreads), 0, s, p, mode, x_vec, \
+#define MOE_STREAM(VEC)                                                                                        \
+    hipLaunchKernelGGL((mx_stream_kernel<SWIGLU, VEC, INLINE>), grid, dim3(kThreads), 0, s, p, mode, x_vec,    \
                        (int)slots, passes, n_runs, runs, routes, R)
-        if (p.k % 512 == 0 && sp % 16 == 0)
-            MOE_STREAM(2, true);
-        else if (p.k % 256 == 0 && sp % 8 == 0)
-            MOE_STREAM(2, true);
+        if (p.k % 256 == 0 && sp % 8 == 0)
+            MOE_STREAM(true);
         else
-            MOE_STREAM(2, false);
+            MOE_STREAM(false);
 #undef MOE_STREAM
     } else {
         const dim3 grid((cols + kTile - 1) / kTile, (unsigned)slots);
 #define MOE_SPLIT(U, VEC)                                                                                       \
-    hipLaunchKernelGGL((mx_split_kernel<SWIGLU, U, VEC, 1, INLINE>), grid, dim3(kThreads), 0, s, p, mode, x_vec, \
+    hipLaunchKernelGGL((mx_split_kernel<SWIGLU, U, VEC, INLINE>), grid, dim3(kThreads), 0, s, p, mode, x_vec, \
                        n_runs, runs, routes, R)
         if (p.k % 512 == 0 && p.k >= 2048 && sp % 16 == 0)
             MOE_SPLIT(4, true);
@@ -1120,11 +1107,36 @@ hipError_t launch_tile(const MxParams &p, const uint8_t *xc, const uint8_t *xs, 
     return hipGetLastError();
 }
 
-// Routes a run may hold, by the mean number of routes to a row: the widest
-// tile that those fill.
-int run_length_for(int R, int P, bool lists) {
-    const int mean = lists ? R / std::min(R, P) : R;
-    return mean >= 160 ? 256 : mean >= 64 ? 128 : mean >= 24 ? 64 : kTile;
+// Routes a run may hold.  A longer run reads its matrix once for more routes
+// and lets an operand byte from LDS meet more of the other; it costs idle
+// columns where lists are shorter, and blocks.  Measured (us, n x k of one
+// matrix, one product from bf16 x; "lists" are routes spread at random):
+//   16 -> 64: the tile kernel needs a launch of its own before it but keeps
+//     more of the matrix on its way.  67 MB of matrices in question, one
+//     route each: 16.1 / 18.4 (1024 x 2048), 17.1 / 23.0 (2048 x 512), 18.5
+//     / 16.5 (4096 x 4096); 100 MB 27.5 / 26.7; 134 MB 35.0 / 29.4; 33 MB
+//     12.6 / 16.2.  By the mean, at 42 MB: 8 routes 16.0 / 18.8, 12 19.8 /
+//     19.2, 16 28.8 / 19.3.  One matrix has no list longer than the mean:
+//     32 routes 12.7 / 14.8, 48 18.0 / 16.3.
+//   64 -> 128: mean 48 22.0 / 23.6, 56 26.9 / 24.0, 64 30.1 / 24.4; fewer
+//     blocks than CUs: 256 routes of one 8192 x 4096 28.1 / 33.0, 1024 (512
+//     blocks) 53.6 / 39.5.
+//   128 -> 256 (32 matrices, 2048 rows): k 4096 mean 256 101 / 109, 512 168
+//     / 164, 1024 294 / 277; k 1024 mean 512 69 / 77; one 8192 x 4096, 1024
+//     routes (128 blocks) 39.5 / 51.5, 4096 (512) 141 / 111.
+int run_length_for(const MxParams &p, int R) {
+    constexpr int64_t kMuch = 80 << 20;      // bytes of matrices in question
+    constexpr int kCus = 256;
+    const bool lists = p.idx != nullptr;
+    const int matrices = lists ? std::min(R, p.P) : 1, mean = R / matrices;
+    auto blocks = [&](int len) {
+        const int rows = tile_rows(len);
+        return std::max<int64_t>(matrices, R / len) * ((p.n + rows - 1) / rows);
+    };
+    if (mean >= 384 && p.k >= 2048 && blocks(256) >= kCus) return 256;
+    if (mean >= 56 && blocks(128) >= kCus) return 128;
+    if (mean >= (lists ? 12 : 48) || (int64_t)matrices * p.n * p.k / 2 >= kMuch) return 64;
+    return kTile;
 }
 
 template <typename OUT>
@@ -1138,7 +1150,7 @@ hipError_t launch_tile_for(int run_length, const MxParams &p, const uint8_t *xc,
 
 }  // namespace
 
-hipError_t launch_mx_product(const MxParams &p, bool reuse_lists, hipStream_t s) {
+hipError_t launch_mx_product(const MxParams &p, int *list_length, hipStream_t s) {
     const int R = p.T * p.K;
     if (R == 0) return hipSuccess;
     const MxWs L = mx_ws(p.P, p.k, p.T, p.K);
@@ -1146,7 +1158,7 @@ hipError_t launch_mx_product(const MxParams &p, bool reuse_lists, hipStream_t s)
     Run *runs = reinterpret_cast<Run *>(p.ws + L.runs);
     int32_t *routes = reinterpret_cast<int32_t *>(p.ws + L.routes);
     uint8_t *xc = p.ws + L.codes, *xs = p.ws + L.scales;
-    const int run_length = run_length_for(R, p.P, p.idx != nullptr);
+    const int run_length = run_length_for(p, R);
     const bool stream = run_length == kTile;
     if (p.idx != nullptr && stream && R <= kInlineRoutes) {
         const bool by_route = R <= p.P;
@@ -1154,7 +1166,7 @@ hipError_t launch_mx_product(const MxParams &p, bool reuse_lists, hipStream_t s)
                              by_route ? R : p.P + 1, s);
     }
     // lists of routes, and x quantised where a tile kernel reads it
-    const int lists = p.idx != nullptr && !reuse_lists;
+    const int lists = p.idx != nullptr && *list_length != run_length;
     if (lists || !stream) {
         PrepareParams a{.idx = p.idx,
                         .R = R,
@@ -1191,6 +1203,7 @@ hipError_t launch_mx_product(const MxParams &p, bool reuse_lists, hipStream_t s)
             hipLaunchKernelGGL(mx_prepare_kernel<false>, dim3(grid), dim3(kGroupThreads), lds, s, a);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
+        if (lists) *list_length = run_length;
     }
     int64_t max_runs = (R + run_length - 1) / run_length;
     if (p.idx != nullptr)

@@ -373,10 +373,11 @@ struct MxParams {
 };
 size_t mx_workspace_bytes(int P, int n, int k, int T, int K);
 constexpr int kMxMaxRows = 32768, kMxMaxRoutes = 131072, kMxMaxN = 1 << 20, kMxMaxK = 1 << 16;
-// The lists of routes by row depend on idx alone: a second product over the
-// same idx, T K and P may reuse those a first one left in the workspace
-// (reuse_lists, same T K and P), with its own T and K split.
-hipError_t launch_mx_product(const MxParams &p, bool reuse_lists, hipStream_t s);
+// *list_length: the run length of the lists of routes by row that the
+// workspace holds, 0 for none, and of those it holds afterwards.  They depend
+// on idx alone: a second product over the same idx, P and T K, with its own T
+// and K split, takes a first one's lists where it wants runs of that length.
+hipError_t launch_mx_product(const MxParams &p, int *list_length, hipStream_t s);
 
 // The single-token layer step in two launches: stage 1 = miss gather
 // (+ the fetched experts' gate/up dots into gu [plan][2F]) | shared gate/up

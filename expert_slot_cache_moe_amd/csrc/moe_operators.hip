@@ -207,7 +207,8 @@ moe_status_t moe_mx_product(const moe_mx_bank_t *bank, const void *x, int64_t x_
     p.out_type = out_type;
     p.out = out;
     p.ws = static_cast<uint8_t *>(ws);
-    HIP_TRY(launch_mx_product(p, false, static_cast<hipStream_t>(stream)), "MXFP4 product launch");
+    int lists = 0;
+    HIP_TRY(launch_mx_product(p, &lists, static_cast<hipStream_t>(stream)), "MXFP4 product launch");
     return MOE_OK;
 }
 
@@ -257,7 +258,8 @@ moe_status_t moe_routed_decode_mx(const moe_pool_t *pool, const void *x, const i
     p.out_type = MOE_TYPE_BF16;
     p.out = h;
     p.ws = base;
-    HIP_TRY(launch_mx_product(p, false, s), "gate/up product launch");
+    int lists = 0;
+    HIP_TRY(launch_mx_product(p, &lists, s), "gate/up product launch");
     p.codes = static_cast<const uint8_t *>(pool->banks_dev[2]);
     p.scales = static_cast<const uint8_t *>(pool->banks_dev[3]);
     p.n = H;
@@ -269,7 +271,7 @@ moe_status_t moe_routed_decode_mx(const moe_pool_t *pool, const void *x, const i
     p.swiglu = 0;
     p.out_type = MOE_TYPE_F32;
     p.out = d;
-    HIP_TRY(launch_mx_product(p, true, s), "down product launch");
+    HIP_TRY(launch_mx_product(p, &lists, s), "down product launch");
     HIP_TRY(launch_combine(idx, w, T, K, H, P, d, addend, static_cast<uint16_t *>(out), s), "combine launch");
     return MOE_OK;
 }

@@ -435,6 +435,35 @@ def test_product_of_one_long_list_among_empty_ones(T, P, n, k):
     _check_product(bank, codes, scales, x, idx, True, torch.bfloat16)
 
 
+# runs of 16 from prepared lists (the waves split k, or do not), of 64 for much matrix and few
+# routes, of 128 and of 256, with scales in single bytes, dwords and vectors
+@pytest.mark.parametrize("T,K,P,n,k,swiglu,out_dtype", [
+    (700, 3, 200, 100, 160, False, torch.float32), (700, 3, 200, 100, 512, True, torch.bfloat16),
+    (350, 6, 200, 700, 256, True, torch.float32), (350, 6, 200, 699, 160, False, torch.bfloat16),
+    (4, 6, 30, 2048, 4096, True, torch.bfloat16), (1, 40, 40, 1999, 2112, False, torch.float32),
+    (1150, 2, 40, 901, 352, False, torch.float32), (1150, 2, 40, 898, 384, True, torch.bfloat16),
+    (1150, 2, 40, 900, 512, True, torch.float32), (1200, 2, 40, 896, 32, False, torch.bfloat16),
+    (800, 1, 2, 22010, 2080, False, torch.float32), (800, 1, 2, 21904, 2176, True, torch.bfloat16),
+    (800, 1, 2, 21906, 2560, True, torch.float32), (800, 1, 2, 21904, 2048, False, torch.bfloat16),
+])
+def test_product_of_every_run_length(T, K, P, n, k, swiglu, out_dtype):
+    _say("run length", T, K, P, n, k, swiglu, out_dtype)
+    g = W.rng(20, "runs", T, K, P, n, k)
+    bank, codes, scales = _bank(g, P, n, k)
+    x = torch.from_numpy(W.normal_bf16(g, (T, k)).view(np.int16)).cuda().view(torch.bfloat16)
+    _check_product(bank, codes, scales, x, _idx(g, T, K, P, 0.02), swiglu, out_dtype)
+
+
+@pytest.mark.parametrize("T,n,k", [(20, 22000, 32), (30, 16500, 416), (47, 40, 608), (50, 40, 608), (1100, 16200, 2080),
+                                   (1025, 4150, 96)])
+def test_dense_product_of_every_run_length(T, n, k):
+    _say("dense run length", T, n, k)
+    g = W.rng(21, "dense runs", T, n, k)
+    bank, codes, scales = _bank(g, 1, n, k)
+    x = torch.from_numpy(W.normal_bf16(g, (T, k)).view(np.int16)).cuda().view(torch.bfloat16)
+    _check_product(bank, codes, scales, x, None, False, torch.float32)
+
+
 @pytest.mark.parametrize("T,n,k", [(1, 70, 96), (16, 16, 128), (100, 300, 640), (257, 129, 256), (1000, 64, 2048)])
 def test_dense_product_without_ids(T, n, k):
     g = W.rng(19, "dense", T, n, k)
@@ -680,6 +709,33 @@ def test_routed_mx_is_route_product_product_combine(T, K, P, H, F, with_addend):
     assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + slack).all()
     if T > 2 and add is None:
         assert (out[1] == 0).all()
+
+
+@pytest.mark.parametrize("T,K,P,H,F", [(4, 6, 30, 2048, 2048), (300, 8, 300, 640, 512), (800, 2, 4, 2048, 11008)])
+def test_routed_mx_with_runs_of_two_lengths(T, K, P, H, F):
+    # the down product's half as large matrices are taken in runs of another length than the
+    # gate/up product's: the lists are made anew, and the result is that of the two alone
+    _say("routed mx, two lengths", T, K, P, H, F)
+    g = W.rng(54, "two lengths", T, K, P, H, F)
+    banks = [torch.from_numpy(g.integers(*r, s, dtype=np.uint8)).cuda().view(-1) for r, s in (
+        ((0, 256), (P, 2 * F, H // 2)), ((110, 122), (P, 2 * F, H // 32)), ((0, 256), (P, H, F // 2)),
+        ((110, 122), (P, H, F // 32)))]
+    pool = m.make_pool(m.MOE_FMT_MXFP4, H, F, P, banks)
+    x = torch.from_numpy(W.normal_bf16(g, (T, H)).view(np.int16)).cuda().view(torch.bfloat16)
+    ids = torch.from_numpy(_idx(g, T, K, P, 0.02)).cuda()
+    w = torch.from_numpy(g.random((T, K), dtype=np.float32)).cuda()
+    out = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((m.moe_routed_mx_workspace_bytes(P, H, F, T, K),), 0xFF, dtype=torch.uint8, device="cuda")
+    m.moe_routed_decode_mx(pool, x, ids, w, out, ws)
+    up = m.make_mx_bank(banks[0].view(P, 2 * F, H // 2), banks[1].view(P, 2 * F, H // 32))
+    dn = m.make_mx_bank(banks[2].view(P, H, F // 2), banks[3].view(P, H, F // 32))
+    h = _product(up, x, ids, swiglu=True)
+    y = _product(dn, h, ids.view(-1, 1), out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    want = _combine(y.cpu().numpy(), ids.cpu().numpy(), w.cpu().numpy(), None, P)
+    # fp32 chain against one double-rounded step each: K steps of 2^-24 of the largest partial sum
+    slack = (K + 1) * 2.0 ** -23 * np.abs(w.cpu().numpy()[:, :, None] * y.cpu().numpy().reshape(T, K, H)).sum(1)
+    assert (np.abs(_f64(out) - want) <= 2.0 ** -8 * np.abs(want) + slack).all()
 
 
 def test_routed_mx_is_near_the_16_bit_activations():
