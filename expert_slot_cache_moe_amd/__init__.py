@@ -517,6 +517,8 @@ def moe_layer_decode_router(cache: Cache, layer: int, x, logits, K: int, out, ro
     T = x.shape[0]
     if router is not None:
         _check_bias(router, cache.E)
+        _on_current_device(x, logits, out, ids_out, w_out)
+        _want(logits, "logits", (T, cache.E), _F32)
     _check(lib().moe_layer_decode_router(
         cache.handle, layer, _dev_ptr(x), _dev_ptr(logits), T, K,
         C.byref(router) if router is not None else None,
@@ -584,7 +586,7 @@ def moe_mx_product(bank: moe_mx_bank_t, x, idx, out, workspace, swiglu: bool = F
     """x [T, k] bfloat16 (rows may be strided), idx int32 [T, K] or None,
     out [T * K, n or n/2] float32 or bfloat16."""
     T, k, stride = _rows_of(x, "x")
-    dev = _on_current_device(x, idx, out, workspace, *bank._keep)
+    dev = _on_current_device(x, idx, out, workspace, *getattr(bank, "_keep", ()))
     if k != bank.k:
         raise ValueError(f"x has {k} columns, the bank's matrices {bank.k}")
     if _type_of(x, "x") != MOE_TYPE_BF16:

@@ -226,7 +226,7 @@ __global__ __launch_bounds__(kGroupThreads) void mx_prepare_kernel(PrepareParams
 
 constexpr int kWaves = 4, kThreads = kWaves * kWave;
 
-// Short runs: 16 NT routes of one matrix row at a time against columns of
+// Short runs: 16 routes of one matrix row at a time against columns of
 // 16, the matrix straight from memory to registers (it is read once, so
 // nothing is gained by passing it through LDS), x quantised where it is
 // needed, so that no launch of its own has to do that first.
@@ -236,8 +236,9 @@ constexpr int kWaves = 4, kThreads = kWaves * kWave;
 //   kByRoute slot r is route r: the first route of its matrix row takes all
 //            of that row's routes, the others leave;
 //   kByRow   slot i is matrix row i, slot P the routes without a row.
-// The last two look through idx in the block itself: few routes, no launch
-// for the lists.
+// The last two look through idx in the block itself: no launch for the lists,
+// but every block reads all ids.  1200 routes over 160 matrices 15.7 us, from
+// prepared lists 19.7; 2000 over 256 77.9 and 75.9: up to 2048.
 enum ListMode : int { kRuns, kByRoute, kByRow };
 constexpr int kInlineRoutes = 2048, kIdxPerThread = kInlineRoutes / kThreads;
 static_assert(kIdxPerThread * kWaves <= kWave, "one lane for each count");
@@ -454,6 +455,9 @@ template <int U, bool VEC, int kM> struct MatrixChunk {
 // SwiGLU 16 gate and 16 up rows) and split k, every fourth chunk of U steps
 // each; their sums are added in LDS, in wave order.  A lane's part of x for
 // one step is one whole MX block of one token, quantised in registers.
+//
+// A token's 8 routes of 1024 x 2048 (9 MB) take 5.6 us: 3.3 of an empty
+// launch, then the latency of ids, matrix and sums one behind the other.
 template <bool SWIGLU, int U, bool VEC, bool INLINE>
 __global__ __launch_bounds__(kThreads) void mx_split_kernel(MxParams p, int mode, bool x_vec,
                                                             const int32_t *__restrict__ n_runs,
@@ -548,6 +552,11 @@ __global__ __launch_bounds__(kThreads) void mx_split_kernel(MxParams p, int mode
 // first and the matrix behind it: x is quantised while the matrix, two
 // chunks of U steps at once, is on its way.  Where those are all of k they
 // serve every pass over a long list.
+//
+// 1280 routes spread over 160 matrices of 512 x 1024 (45 MB) take 16 us, 2.8
+// TB/s: bound by latency, as the blocks of a launch ask for their ids, their
+// x and their matrix in turn, and all end within 10 us.  Skewed lists (the
+// longest of 50 routes) take 20.
 constexpr int kSpanBlocks = 64;
 
 template <bool SWIGLU, bool VEC, bool INLINE>
@@ -702,10 +711,17 @@ __global__ __launch_bounds__(kThreads, 3) void mx_stream_kernel(MxParams p, int 
 // chunks (one MX block each); chunk j lies in slot j ^ (row / 2 % 8): two rows
 // fill the 64 banks, and the 16 rows that are read at once hit each bank once.
 constexpr int kStageBlocks = 8, kStageBytes = 16 * kStageBlocks;
-// Rows of the matrix a block takes: at BT 256 as many as the registers hold
-// (two thirds of the device's rate need 128 rows for an operand byte); below,
-// where the matrix's bytes bound the kernel, few enough for two blocks on a
-// CU, so that one asks for memory while the other multiplies.
+// Rows of the matrix a block takes: at BT 256 as many as the registers hold;
+// below, where the matrix's bytes bound the kernel, few enough for two blocks
+// on a CU, so that one asks for memory while the other multiplies.
+//
+// 8192 rows of x times one 4096 x 4096 matrix take 86 us at BT 256 (3.2
+// PFLOP/s; the instructions alone would take 27): two blocks follow each
+// other on a CU, and the first stage's requests, the results' way out and the
+// operand reads that the products do not cover stand beside the products.
+// 24576 routes over 256 matrices of 2048 x 4096 (1.1 GB) take 310 us at BT
+// 128, 3.7 TB/s: bound by the matrices' bytes, of which two blocks on a CU
+// keep 64 KB on their way.
 constexpr int tile_rows(int bt) { return bt == 256 ? 256 : 128; }
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -1031,9 +1047,14 @@ size_t mx_workspace_bytes(int P, int n, int k, int T, int K) {
 namespace {
 
 // Blocks of the many-block form that keep the device busy; with fewer, k is
-// split over the waves instead.
+// split over the waves instead (split / many, us: 64 blocks 4.7 / 9.1, 256
+// 11.3 / 10.7, 320 8.4 / 9.9, 384 27.5 / 32.0, 512 19.6 / 15.2 and 24.9 /
+// 16.4, 1024 33.9 / 33.0).
 constexpr int64_t kManyBlocks = 512;
-// Blocks for the passes over one matrix row's list, where lists may be long.
+// Blocks for the passes over one matrix row's list, where lists may be long:
+// the longest list of a skewed batch is the kernel's last block.  1200 routes
+// over 160 matrices of 512 x 1024 in 1, 2, 4 blocks (us): evenly spread 15.4
+// 15.8 19.2, 50 more on one matrix 26.3 19.4 19.8, 200 67.8 39.5 28.8.
 constexpr int kPassBlocks = 2;
 
 template <bool SWIGLU, bool INLINE>
@@ -1059,6 +1080,8 @@ hipError_t launch_stream_shape(const MxParams &p, int mode, const int32_t *n_run
 #define MOE_SPLIT(U, VEC)                                                                                       \
     hipLaunchKernelGGL((mx_split_kernel<SWIGLU, U, VEC, INLINE>), grid, dim3(kThreads), 0, s, p, mode, x_vec, \
                        n_runs, runs, routes, R)
+        // four steps at once where each of the four waves has that many (2 / 4
+        // steps, us: k 2048 5.13 / 4.85, 4096 6.65 / 6.20, 8192 10.1 / 9.5)
         if (p.k % 512 == 0 && p.k >= 2048 && sp % 16 == 0)
             MOE_SPLIT(4, true);
         else if (p.k % 256 == 0 && sp % 8 == 0)
@@ -1139,6 +1162,12 @@ int run_length_for(const MxParams &p, int R) {
     return kTile;
 }
 
+// Runs the lists may hold.
+int64_t max_runs_of(const MxParams &p, int R, int run_length) {
+    return p.idx != nullptr ? std::min<int64_t>(R, (int64_t)p.P + 1) + R / run_length
+                            : (R + run_length - 1) / run_length;
+}
+
 template <typename OUT>
 hipError_t launch_tile_for(int run_length, const MxParams &p, const uint8_t *xc, const uint8_t *xs,
                            const int32_t *n_runs, const Run *runs, const int32_t *routes, int R,
@@ -1149,6 +1178,18 @@ hipError_t launch_tile_for(int run_length, const MxParams &p, const uint8_t *xc,
 }
 
 }  // namespace
+
+bool mx_launchable(const MxParams &p) {
+    const int R = p.T * p.K;
+    if (R == 0) return true;
+    const int run_length = run_length_for(p, R);
+    const int cols = p.swiglu ? p.n / 2 : p.n;
+    // (the short runs' narrowest block that comes in numbers: a wave's columns times four)
+    const int width = run_length == kTile ? kWaves * (p.swiglu ? 1 : 2) * kTile
+                                          : tile_rows(run_length) / (p.swiglu ? 2 : 1);
+    const int64_t tiles = (cols + width - 1) / width;
+    return (max_runs_of(p, R, run_length) + 8) * tiles * kPassBlocks <= (int64_t)UINT32_MAX / kThreads;
+}
 
 hipError_t launch_mx_product(const MxParams &p, int *list_length, hipStream_t s) {
     const int R = p.T * p.K;
@@ -1205,11 +1246,8 @@ hipError_t launch_mx_product(const MxParams &p, int *list_length, hipStream_t s)
         if (e != hipSuccess) return e;
         if (lists) *list_length = run_length;
     }
-    int64_t max_runs = (R + run_length - 1) / run_length;
-    if (p.idx != nullptr)
-        max_runs = std::min<int64_t>(R, (int64_t)p.P + 1) + R / run_length;
-    else
-        n_runs = nullptr;
+    const int64_t max_runs = max_runs_of(p, R, run_length);
+    if (p.idx == nullptr) n_runs = nullptr;
     if (stream) return launch_stream(p, kRuns, n_runs, runs, routes, R, max_runs, s);
     return p.out_type == MOE_TYPE_F32
                ? launch_tile_for<float>(run_length, p, xc, xs, n_runs, runs, routes, R, max_runs, s)

@@ -9,12 +9,19 @@
 // A lane holds experts lane, lane + 64, ... of the row.  Choice values are
 // first formed in fp32, where their error is bounded; the K-th largest of
 // the 64 lanes' own maxima, less that bound, is a floor that every pick
-// reaches and few others do (measured: 11 to 12 candidates for 10 picks of
-// 512).  The candidates are packed one to a lane, their values computed in
-// 64 bits, and their ranks counted.  Where more than 64 values reach the
-// floor (rows of equal scores), or two groups at the border of the choice
-// are closer than the bound, the row takes the long way: every value in 64
-// bits, K rounds of a wave maximum.
+// reaches and few others do.  The candidates are packed one to a lane, their
+// values computed in 64 bits, and their ranks counted.  Where more than 64
+// values reach the floor (rows of equal scores), or two groups at the border
+// of the choice are closer than the bound, the row takes the long way: every
+// value in 64 bits, K rounds of a wave maximum.
+//
+// On MI355X one row of 256 grouped experts takes 4.8 us, of which 3.3 are an
+// empty launch; 16384 rows of 512 (33.5 MB) 21 us, where reading them takes
+// 7: bound by the instructions of a row (exponentials, ballots and the 64-bit
+// ranks of a dozen candidates), of which the waves of a SIMD issue one a
+// cycle.  The long way for every row took 95.  Four rows to a wave, whose
+// serial parts overlap but whose registers allow fewer waves, took 21.3 at
+// 512 experts and 12.2 (one row: 10.8) at 256.
 #include "moe_internal.h"
 
 namespace moe {

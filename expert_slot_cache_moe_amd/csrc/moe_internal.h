@@ -341,7 +341,7 @@ struct RouteParams {
     int32_t log_groups;
     uint32_t group_magic;
 };
-constexpr int kRouteMaxExperts = 2048, kRouteMaxGroups = 64;
+constexpr int kRouteMaxExperts = 2048, kRouteMaxGroups = 64, kRouteMaxRows = 1 << 24;
 hipError_t launch_route(const RouteParams &p, int logits_type, const void *logits, int64_t stride, int T,
                         int E, int K, int32_t *ids, float *w, hipStream_t s);
 
@@ -373,6 +373,8 @@ struct MxParams {
 };
 size_t mx_workspace_bytes(int P, int n, int k, int T, int K);
 constexpr int kMxMaxRows = 32768, kMxMaxRoutes = 131072, kMxMaxN = 1 << 20, kMxMaxK = 1 << 16;
+// false: a grid's threads would pass the 32 bits that count them.
+bool mx_launchable(const MxParams &p);
 // *list_length: the run length of the lists of routes by row that the
 // workspace holds, 0 for none, and of those it holds afterwards.  They depend
 // on idx alone: a second product over the same idx, P and T K, with its own T

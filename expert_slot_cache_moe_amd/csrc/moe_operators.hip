@@ -128,6 +128,7 @@ moe_status_t moe_route(const moe_router_t *router, int32_t logits_type, const vo
     if (T < 0 || E < 1 || K < 1 || K > E || K > kMaxTopK)
         return fail(MOE_INVALID_ARG, "bad routing sizes T=%d E=%d K=%d", T, E, K);
     if (stride < E) return fail(MOE_INVALID_ARG, "row stride %lld < E=%d", (long long)stride, E);
+    if (T > kRouteMaxRows) return fail(MOE_UNSUPPORTED, "T=%d > %d", T, kRouteMaxRows);
     RouteParams p;
     moe_status_t st = check_router(router, E, p);
     if (st != MOE_OK) return st;
@@ -207,6 +208,7 @@ moe_status_t moe_mx_product(const moe_mx_bank_t *bank, const void *x, int64_t x_
     p.out_type = out_type;
     p.out = out;
     p.ws = static_cast<uint8_t *>(ws);
+    if (!mx_launchable(p)) return fail(MOE_UNSUPPORTED, "%d routes of %d x %d: too many tiles", T * K, p.n, p.k);
     int lists = 0;
     HIP_TRY(launch_mx_product(p, &lists, static_cast<hipStream_t>(stream)), "MXFP4 product launch");
     return MOE_OK;
@@ -243,35 +245,38 @@ moe_status_t moe_routed_decode_mx(const moe_pool_t *pool, const void *x, const i
     uint8_t *base = static_cast<uint8_t *>(ws);
     uint16_t *h = reinterpret_cast<uint16_t *>(base + L.h);
     float *d = reinterpret_cast<float *>(base + L.d);
-    MxParams p{};
-    p.codes = static_cast<const uint8_t *>(pool->banks_dev[0]);
-    p.scales = static_cast<const uint8_t *>(pool->banks_dev[1]);
-    p.P = P;
-    p.n = 2 * F;
-    p.k = H;
-    p.x = static_cast<const uint16_t *>(x);
-    p.x_stride = H;
-    p.idx = idx;
-    p.T = T;
-    p.K = K;
-    p.swiglu = 1;
-    p.out_type = MOE_TYPE_BF16;
-    p.out = h;
-    p.ws = base;
+    MxParams up{}, down{};
+    up.codes = static_cast<const uint8_t *>(pool->banks_dev[0]);
+    up.scales = static_cast<const uint8_t *>(pool->banks_dev[1]);
+    up.P = P;
+    up.n = 2 * F;
+    up.k = H;
+    up.x = static_cast<const uint16_t *>(x);
+    up.x_stride = H;
+    up.idx = idx;
+    up.T = T;
+    up.K = K;
+    up.swiglu = 1;
+    up.out_type = MOE_TYPE_BF16;
+    up.out = h;
+    up.ws = base;
+    down = up;
+    down.codes = static_cast<const uint8_t *>(pool->banks_dev[2]);
+    down.scales = static_cast<const uint8_t *>(pool->banks_dev[3]);
+    down.n = H;
+    down.k = F;
+    down.x = h;
+    down.x_stride = F;
+    down.T = T * K;   // a row of h for each route
+    down.K = 1;
+    down.swiglu = 0;
+    down.out_type = MOE_TYPE_F32;
+    down.out = d;
+    if (!mx_launchable(up) || !mx_launchable(down))
+        return fail(MOE_UNSUPPORTED, "%d routes of hidden %d, ffn %d: too many tiles", T * K, H, F);
     int lists = 0;
-    HIP_TRY(launch_mx_product(p, &lists, s), "gate/up product launch");
-    p.codes = static_cast<const uint8_t *>(pool->banks_dev[2]);
-    p.scales = static_cast<const uint8_t *>(pool->banks_dev[3]);
-    p.n = H;
-    p.k = F;
-    p.x = h;
-    p.x_stride = F;
-    p.T = T * K;   // a row of h for each route
-    p.K = 1;
-    p.swiglu = 0;
-    p.out_type = MOE_TYPE_F32;
-    p.out = d;
-    HIP_TRY(launch_mx_product(p, &lists, s), "down product launch");
+    HIP_TRY(launch_mx_product(up, &lists, s), "gate/up product launch");
+    HIP_TRY(launch_mx_product(down, &lists, s), "down product launch");
     HIP_TRY(launch_combine(idx, w, T, K, H, P, d, addend, static_cast<uint16_t *>(out), s), "combine launch");
     return MOE_OK;
 }

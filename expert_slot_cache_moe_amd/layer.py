@@ -80,7 +80,9 @@ class SlotCacheLayers:
                 w13, w2, gate = (torch.from_numpy(np.ascontiguousarray(a).view(np.int16)).to(self.device)
                                  for a in shared[l])
                 self.shared.append(make_shared(w13, w2, gate, ffn=w2.numel() // hidden))
-        self.routers = router if isinstance(router, (list, tuple)) else [router] * layers
+        self.routers = list(router) if isinstance(router, (list, tuple)) else [router] * layers
+        if len(self.routers) != layers:
+            raise ValueError(f"{len(self.routers)} routers for {layers} layers")
         if max_routes is None:
             max_routes = max(max_tokens * max_top_k, 1)
         self.cache = moe_cache_create(
@@ -107,6 +109,8 @@ class SlotCacheLayers:
 
     def decode_hybrid(self, layer, x, logits, K, out, ids_out=None, w_out=None, max_fetch=-1,
                       stream=None):
+        if any(r is not None for r in self.routers):
+            raise ValueError("the hybrid step routes by softmax top-k; it takes no router")
         sh = self._shared(layer)
         moe_layer_decode_hybrid(self.cache, layer, x, logits, K, out, shared=sh, max_fetch=max_fetch,
                                 ids_out=ids_out, w_out=w_out, stream=stream)

@@ -456,7 +456,7 @@ typedef struct {
  * ids_dev: int32 [T][K]; w_dev: fp32 [T][K].  Asynchronous, capturable.
  * Errors: MOE_INVALID_ARG (T < 0, K < 1, K > E, K > 64, bad router fields,
  * a stride below E, null pointers), MOE_UNSUPPORTED (E > 2048, more than
- * 64 groups). */
+ * 64 groups, T > 2^24). */
 moe_status_t moe_route(const moe_router_t *router, int32_t logits_type, const void *logits_dev,
                        int64_t row_stride, int32_t T, int32_t E, int32_t K, int32_t *ids_dev,
                        float *w_dev, void *stream);
@@ -534,7 +534,8 @@ int64_t moe_mx_product_workspace_bytes(int32_t num_rows, int32_t n, int32_t k, i
  * overwritten; calls that share it must be ordered.  Asynchronous,
  * capturable.  Errors: MOE_INVALID_ARG (sizes, strides, null or misaligned
  * pointers, workspace too small), MOE_UNSUPPORTED (num_rows > 32768, T K >
- * 131072, K > 64, n > 2^20, k > 2^16). */
+ * 131072, K > 64, n > 2^20, k > 2^16, or num_rows, T K and n together so
+ * large that a launch would have 2^32 threads). */
 moe_status_t moe_mx_product(const moe_mx_bank_t *bank, const void *x_dev, int64_t x_stride,
                             const int32_t *idx_dev, int32_t T, int32_t K, int32_t swiglu,
                             int32_t out_type, void *out_dev, void *workspace_dev,

@@ -31,7 +31,7 @@ def _route(router=None, type=0, logits=P, stride=256, T=4, E=256, K=8, ids=P, w=
     (dict(T=-1), 1), (dict(E=0, K=1), 1), (dict(K=0), 1), (dict(K=65), 1), (dict(E=4, K=5), 1),
     (dict(stride=255), 1), (dict(type=2), 1), (dict(type=-1), 1), (dict(logits=None), 1), (dict(ids=None), 1),
     (dict(w=None), 1), (dict(logits=P + 2), 1), (dict(type=1, logits=P + 1), 1), (dict(ids=P + 2), 1),
-    (dict(E=2049, stride=2049), 2), (dict(router=_router(score=2)), 1),
+    (dict(E=2049, stride=2049), 2), (dict(T=(1 << 24) + 1), 2), (dict(router=_router(score=2)), 1),
     (dict(router=_router(num_groups=7)), 1), (dict(router=_router(num_groups=0)), 1),
     (dict(router=_router(num_groups=8, top_groups=9)), 1), (dict(router=_router(num_groups=8, top_groups=0)), 1),
     (dict(router=_router(num_groups=128, top_groups=2)), 2), (dict(router=_router(group_score=2)), 1),
@@ -94,6 +94,9 @@ def _product(bank=None, x=P, stride=64, idx=P, T=2, K=2, swiglu=0, type=1, out=P
     (dict(stride=63), 1), (dict(idx=None), 1), (dict(idx=None, K=1), 1), (dict(x=None), 1), (dict(out=None), 1),
     (dict(ws=None), 1), (dict(x=P + 1), 1), (dict(out=P + 1), 1), (dict(type=0, out=P + 2), 1),
     (dict(idx=P + 2), 1), (dict(ws=P + 128), 1), (dict(ws_bytes=16), 1),
+    # 40961 runs of 16384 blocks, 33281 of 2048: 2^32 threads and more
+    (dict(bank=_bank(num_rows=32768, n=1 << 20, k=32), T=65536), 2),
+    (dict(bank=_bank(num_rows=32768, n=1 << 18, k=4096), stride=4096, T=16384), 2),
 ])
 def test_product_refuses(kw, status):
     assert _product(**kw) == status
@@ -123,6 +126,8 @@ def _routed(pool=None, x=P, idx=P, w=P, T=2, K=2, add=None, out=P, ws=P, ws_byte
     (dict(pool=_pool(bank=P + 8)), 1), (dict(T=-1), 1), (dict(K=0), 1), (dict(T=65536, K=1), 2), (dict(x=None), 1),
     (dict(x=P + 8), 1), (dict(idx=None), 1), (dict(w=None), 1), (dict(out=None), 1), (dict(ws=None), 1),
     (dict(ws=P + 64), 1), (dict(ws_bytes=100), 1), (dict(add=P + 2), 1), (dict(out=P + 1), 1),
+    (dict(pool=_pool(rows=32768, H=32, F=1 << 18), T=32768, ws_bytes=1 << 50), 2),
+    (dict(pool=_pool(rows=32768, H=1 << 16, F=4096), T=65535, ws_bytes=1 << 50), 2),
 ])
 def test_routed_mx_refuses(kw, status):
     assert _routed(**kw) == status
@@ -145,6 +150,16 @@ def test_workspace_sizes():
 def test_layer_step_with_a_null_cache_is_refused():
     r = _router()
     assert _status("moe_layer_decode_router", None, 0, P, P, 1, 2, C.byref(r), None, -1, P, None, None, None) == 1
+
+
+def test_hybrid_step_refuses_a_router():
+    # the host threads' half routes by the plain top-k: a router must not be dropped in silence
+    from expert_slot_cache_moe_amd.layer import SlotCacheLayers
+
+    lay = object.__new__(SlotCacheLayers)
+    lay.routers = [None, _router(score=m.MOE_SCORE_SIGMOID)]
+    with pytest.raises(ValueError, match="router"):
+        lay.decode_hybrid(0, None, None, 2, None)
 
 
 # ---------------------------------------------------------------- the plain forms
