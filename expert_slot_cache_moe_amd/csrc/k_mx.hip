@@ -456,8 +456,8 @@ template <int U, bool VEC, int kM> struct MatrixChunk {
 // each; their sums are added in LDS, in wave order.  A lane's part of x for
 // one step is one whole MX block of one token, quantised in registers.
 //
-// A token's 8 routes of 1024 x 2048 (9 MB) take 5.6 us: 3.3 of an empty
-// launch, then the latency of ids, matrix and sums one behind the other.
+// A token's 8 routes of 1024 x 2048 (9 MB) take 5.4 us: the latency of ids,
+// matrix and sums one behind the other.
 template <bool SWIGLU, int U, bool VEC, bool INLINE>
 __global__ __launch_bounds__(kThreads) void mx_split_kernel(MxParams p, int mode, bool x_vec,
                                                             const int32_t *__restrict__ n_runs,
@@ -720,8 +720,10 @@ constexpr int kStageBlocks = 8, kStageBytes = 16 * kStageBlocks;
 // other on a CU, and the first stage's requests, the results' way out and the
 // operand reads that the products do not cover stand beside the products.
 // 24576 routes over 256 matrices of 2048 x 4096 (1.1 GB) take 310 us at BT
-// 128, 3.7 TB/s: bound by the matrices' bytes, of which two blocks on a CU
-// keep 64 KB on their way.
+// 128, 3.7 TB/s: bound by the matrices' bytes and, from L2, the routes'.  At
+// BT 64, one route to each of some 200 of them take 152 us, 5.7 TB/s.
+// A second stage on its way to registers took 379 us (BT 128, for want of
+// registers) and 150 (BT 64; 21.3 for 20.8 where 45 MB are read).
 constexpr int tile_rows(int bt) { return bt == 256 ? 256 : 128; }
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 

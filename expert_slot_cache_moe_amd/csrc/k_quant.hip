@@ -15,8 +15,8 @@
 //
 // Bound by memory: a 134M element bf16 matrix (340 MB of both sides) to
 // MXFP4 takes 70 us on MI355X, back 62 us (4.9 and 5.4 TB/s; a large copy
-// reaches 4.9); to E2M1 79 us, bound by the quotients, back 76 us.  One row
-// of 2048 takes 4 us either way, a launch.
+// reaches 4.9); to E2M1 78 us, bound by the quotients, back 74 us.  One row
+// of 2048 takes 1.4 us either way, less than its launch.
 #include "k_rows.inc"
 
 namespace moe {

@@ -15,9 +15,9 @@
 // of the choice are closer than the bound, the row takes the long way: every
 // value in 64 bits, K rounds of a wave maximum.
 //
-// On MI355X one row of 256 grouped experts takes 4.8 us, of which 3.3 are an
-// empty launch; 16384 rows of 512 (33.5 MB) 21 us, where reading them takes
-// 7: bound by the instructions of a row (exponentials, ballots and the 64-bit
+// On MI355X one row of 256 grouped experts takes 4.8 us, the latency of its
+// steps one behind the other; 16384 rows of 512 (33.5 MB) 22 us, where
+// reading them takes 7: bound by the instructions of a row (exponentials, ballots and the 64-bit
 // ranks of a dozen candidates), of which the waves of a SIMD issue one a
 // cycle.  The long way for every row took 95.  Four rows to a wave, whose
 // serial parts overlap but whose registers allow fewer waves, took 21.3 at
