@@ -17,6 +17,7 @@
 // bytes are 0 (2^-127), so what they add is below 2^-240 and rounds to
 // nothing in any sum (fp32 reaches down to 2^-149).
 #include <algorithm>
+#include <type_traits>
 
 #include "k_rows.inc"
 
@@ -553,14 +554,18 @@ __global__ __launch_bounds__(kThreads) void mx_split_kernel(MxParams p, int mode
 // chunks of U steps at once, is on its way.  Where those are all of k they
 // serve every pass over a long list.
 //
-// 1280 routes spread over 160 matrices of 512 x 1024 (45 MB) take 16 us, 2.8
+// 1200 routes spread over 160 matrices of 512 x 1024 (45 MB) take 15 us, 3.0
 // TB/s: bound by latency, as the blocks of a launch ask for their ids, their
 // x and their matrix in turn, and all end within 10 us.  Skewed lists (the
 // longest of 50 routes) take 20.
+//
+// Three waves to a SIMD, though four would fit (three / four, us: 1200 routes
+// over 160 matrices, k 1024 15.3 / 18.8; 80 over 64, k 2048 20.0 / 24.8; 600
+// over 200, k 512 11.3 / 10.3).
 constexpr int kSpanBlocks = 64;
 
 template <bool SWIGLU, bool VEC, bool INLINE>
-__global__ __launch_bounds__(kThreads, 3) void mx_stream_kernel(MxParams p, int mode, bool x_vec, int slots,
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(3, 3))) void mx_stream_kernel(MxParams p, int mode, bool x_vec, int slots,
                                                              int pass_blocks, const int32_t *__restrict__ n_runs,
                                                              const Run *__restrict__ runs,
                                                              const int32_t *__restrict__ routes, int R) {
@@ -622,8 +627,9 @@ __global__ __launch_bounds__(kThreads, 3) void mx_stream_kernel(MxParams p, int 
         ax[m] = p.codes + r * nblk * 16;
         as[m] = p.scales + r * nblk;
     }
-    w[0].load(ax, as, 0, nblk, q);
-    w[1].load(ax, as, min(U, last), nblk, q);
+    auto request = [&](MatrixChunk<U, VEC, kM> &to, int s0) { to.load(ax, as, s0, nblk, q); };
+    request(w[0], 0);
+    request(w[1], min(U, last));
     const bool f32_out = p.out_type == MOE_TYPE_F32;
     const bool whole = cols % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & (f32_out ? 15 : 7)) == 0;
 
@@ -634,8 +640,8 @@ __global__ __launch_bounds__(kThreads, 3) void mx_stream_kernel(MxParams p, int 
         for (int m = 0; m < kM; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
         const int live = min(l.count - base, kTile);
         if (again && steps > 2 * U) {
-            w[0].load(ax, as, 0, nblk, q);
-            w[1].load(ax, as, min(U, last), nblk, q);
+            request(w[0], 0);
+            request(w[1], min(U, last));
         }
         for (int b0 = 0; b0 < nblk; b0 += kSpanBlocks) {
             const int nb = min(kSpanBlocks, nblk - b0);
@@ -662,14 +668,30 @@ __global__ __launch_bounds__(kThreads, 3) void mx_stream_kernel(MxParams p, int 
                     for (int m = 0; m < kM; ++m) acc[m] = mfma(m0.a[m][u], m0.s[m].at(u, q), bv, sb, acc[m]);
                 }
             };
-            for (int s0 = b0 / 4; s0 < s_end; s0 += 2 * U) {
-                chunk(s0, w[0]);
-                if (steps > 2 * U) w[0].load(ax, as, min(s0 + 2 * U, last), nblk, q);
-                if (s0 + U < s_end) {
-                    chunk(s0 + U, w[1]);
-                    if (steps > 2 * U) w[1].load(ax, as, min(s0 + 3 * U, last), nblk, q);
+            // Where the two chunks are not all of k, each is followed by the
+            // request for the chunk after next: behind the products that free
+            // its registers, and on no branch, or the compiler takes other
+            // registers and waits for the requests to copy them.
+            auto multiply = [&](auto whole_k) {
+                for (int s0 = b0 / 4; s0 < s_end; s0 += 2 * U) {
+                    chunk(s0, w[0]);
+                    if constexpr (!decltype(whole_k)::value) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        request(w[0], min(s0 + 2 * U, last));
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    if (s0 + U < s_end) chunk(s0 + U, w[1]);
+                    if constexpr (!decltype(whole_k)::value) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        request(w[1], min(s0 + 3 * U, last));
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
                 }
-            }
+            };
+            if (steps > 2 * U)
+                multiply(std::false_type{});
+            else
+                multiply(std::true_type{});
         }
         if (c < live) {
             const int route = l.route(base + c);
