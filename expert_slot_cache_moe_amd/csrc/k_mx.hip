@@ -556,8 +556,8 @@ __global__ __launch_bounds__(kThreads) void mx_split_kernel(MxParams p, int mode
 //
 // 1200 routes spread over 160 matrices of 512 x 1024 (45 MB) take 15 us, 3.0
 // TB/s: bound by latency, as the blocks of a launch ask for their ids, their
-// x and their matrix in turn, and all end within 10 us.  Skewed lists (the
-// longest of 50 routes) take 20.
+// x and their matrix in turn.  Skewed lists (the longest of 50 routes) take
+// 20: each further pass of a block adds 4.
 //
 // Three waves to a SIMD, though four would fit (three / four, us: 1200 routes
 // over 160 matrices, k 1024 15.3 / 18.8; 80 over 64, k 2048 20.0 / 24.8; 600
@@ -565,10 +565,9 @@ __global__ __launch_bounds__(kThreads) void mx_split_kernel(MxParams p, int mode
 constexpr int kSpanBlocks = 64;
 
 template <bool SWIGLU, bool VEC, bool INLINE>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(3, 3))) void mx_stream_kernel(MxParams p, int mode, bool x_vec, int slots,
-                                                             int pass_blocks, const int32_t *__restrict__ n_runs,
-                                                             const Run *__restrict__ runs,
-                                                             const int32_t *__restrict__ routes, int R) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(3, 3))) void mx_stream_kernel(
+    MxParams p, int mode, bool x_vec, int slots, int pass_blocks, const int32_t *__restrict__ n_runs,
+    const Run *__restrict__ runs, const int32_t *__restrict__ routes, int R) {
     constexpr int kM = 2, U = 2;
     constexpr int kCols = SWIGLU ? kTile : 2 * kTile;       // output columns of a wave
     __shared__ __align__(16) u32x4 xc[kSpanBlocks][kTile];
@@ -782,13 +781,10 @@ template <int N> struct Tiles {
 };
 
 template <int BT, bool SWIGLU, int SVEC, typename OUT>
-__global__ __launch_bounds__(kThreads, BT == 256 ? 1 : 2) void mx_tile_kernel(MxParams p, const uint8_t *__restrict__ xc,
-                                                              const uint8_t *__restrict__ xs,
-                                                              const int32_t *__restrict__ n_runs,
-                                                              const Run *__restrict__ runs,
-                                                              const int32_t *__restrict__ routes, int R,
-                                                              int max_runs, int row_tiles, FastDiv by_K,
-                                                              OUT *__restrict__ out) {
+__global__ __launch_bounds__(kThreads, BT == 256 ? 1 : 2) void mx_tile_kernel(
+    MxParams p, const uint8_t *__restrict__ xc, const uint8_t *__restrict__ xs, const int32_t *__restrict__ n_runs,
+    const Run *__restrict__ runs, const int32_t *__restrict__ routes, int R, int max_runs, int row_tiles,
+    FastDiv by_K, OUT *__restrict__ out) {
     constexpr int kTileRows = tile_rows(BT);
     constexpr int kAcross = BT == 256 ? 2 : 4;       // waves along the rows; the others along the routes
     constexpr int kWaveRows = kTileRows / kAcross, kWaveRoutes = BT * kAcross / kWaves;
