@@ -592,6 +592,94 @@ def test_captured_operators_replay():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T,K,P,n,k", [(300, 2, 20, 130, 288), (1150, 2, 40, 900, 352), (700, 3, 200, 100, 160)])
+def test_captured_product_of_prepared_lists_replays(T, K, P, n, k):
+    g = W.rng(44, "graph lists", T)
+    bank, _, _ = _bank(g, P, n, k)
+    x = torch.zeros((T, k), dtype=torch.bfloat16, device="cuda")
+    idx = torch.zeros((T, K), dtype=torch.int32, device="cuda")
+    y = torch.empty((T * K, n), device="cuda")
+    ws = torch.empty(m.moe_mx_product_workspace_bytes(P, n, k, T, K), dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        m.moe_mx_product(bank, x, idx, y, ws)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.moe_mx_product(bank, x, idx, y, ws)
+    for i in range(4):
+        x.copy_(torch.from_numpy(g.standard_normal((T, k)).astype(np.float32)).to(torch.bfloat16))
+        idx.copy_(torch.from_numpy(_idx(g, T, K, P, 0.3 * i)))
+        if i == 2:
+            idx[:T // 2] = 3                # half of the routes on one matrix
+        y.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        y.fill_(-7.0)
+        m.moe_mx_product(bank, x, idx, y, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(got, y)
+
+
+def test_products_on_two_streams_at_once():
+    g = W.rng(45, "two streams")
+    jobs = []
+    for T, K, P, n, k in ((400, 2, 16, 512, 1024), (45, 3, 24, 515, 1056)):
+        bank, _, _ = _bank(g, P, n, k)
+        x = torch.from_numpy(W.normal_bf16(g, (T, k)).view(np.int16)).cuda().view(torch.bfloat16)
+        idx = torch.from_numpy(_idx(g, T, K, P)).cuda()
+        want = _product(bank, x, idx, out_dtype=torch.float32)
+        out = torch.empty_like(want)
+        ws = torch.empty(m.moe_mx_product_workspace_bytes(P, n, k, T, K), dtype=torch.uint8, device="cuda")
+        jobs.append((bank, x, idx, want, out, ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for bank, x, idx, _, out, ws, s in jobs:
+            m.moe_mx_product(bank, x, idx, out, ws, stream=s)
+    torch.cuda.synchronize()
+    for _, _, _, want, out, _, _ in jobs:
+        assert torch.equal(want, out)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "e2m1"])
+def test_rows_past_32_bit_offsets(fmt):
+    _say("large rows", fmt)
+    rows, cols, B, tail = 2**20 + 77, 4128, 32 if fmt == "mxfp4" else 16, 80   # 4.3e9 elements
+    codes = torch.randint(0, 256, (rows, cols // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.randint(100, 120, (rows, cols // B), dtype=torch.uint8, device="cuda")
+    dst = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    m.moe_dequantize_rows(FMT[fmt], codes, scales, dst)
+    few = torch.empty((tail, cols), dtype=torch.bfloat16, device="cuda")
+    m.moe_dequantize_rows(FMT[fmt], codes[-tail:].contiguous(), scales[-tail:].contiguous(), few)
+    assert torch.equal(dst[-tail:].view(torch.int16), few.view(torch.int16))
+    few_codes, few_scales = torch.empty_like(codes[-tail:]), torch.empty_like(scales[-tail:])
+    m.moe_quantize_rows(FMT[fmt], few, few_codes, few_scales)
+    m.moe_quantize_rows(FMT[fmt], dst, codes, scales)
+    torch.cuda.synchronize()
+    assert torch.equal(codes[-tail:], few_codes) and torch.equal(scales[-tail:], few_scales)
+
+
+def test_product_past_32_bit_offsets():
+    # one scale to a row and x of E2M1 values in blocks of scale 1: terms are multiples of 1/4 of at
+    # most 36, so that their sums are exact in any order, in a bank of few matrices too
+    _say("large bank")
+    P, n, k, few = 1100, 2048, 4096, 24                                        # 4.6 GB of codes
+    assert k * 36 * 4 < 2 ** 24
+    codes = torch.randint(0, 256, (P, n, k // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.randint(100, 140, (P, n, 1), dtype=torch.uint8, device="cuda").expand(P, n, k // 32).contiguous()
+    g = W.rng(46, "large bank")
+    for T, K in ((1, 3), (12, 2), (64, 6)):
+        x = ref.VALUES[g.integers(0, 8, (T, k))] * g.choice([-1.0, 1.0], (T, k))
+        x[:, ::32] = 6.0
+        xt = torch.from_numpy(x).to(torch.bfloat16).cuda()
+        idx = torch.from_numpy(g.integers(0, few, (T, K)).astype(np.int32)).cuda()
+        got = _product(m.make_mx_bank(codes, scales), xt, idx + (P - few), out_dtype=torch.float32)
+        want = _product(m.make_mx_bank(codes[-few:], scales[-few:]), xt, idx, out_dtype=torch.float32)
+        assert torch.equal(got, want) and bool(got.any())
+
+
 def test_operators_run_on_the_given_stream():
     g = W.rng(47, "stream")
     T, P, n, k = 64, 4, 64, 256
