@@ -70,10 +70,13 @@ __device__ __forceinline__ uint32_t e4m3_of(float a, float g) {
     return (uint32_t)min((e + 6) * 8 + q, 0x7E);
 }
 
-// The reciprocal of s g (a scale of 4 bits, g of 24) in two parts.  TRIM: the
-// first part has 16 bits, so that its product with a bf16 number is exact.
-template <bool TRIM> __device__ __forceinline__ void reciprocal(float s, float g, float &ih, float &il) {
+// The reciprocal of u = s g (a scale of 4 bits, g of 24) in two parts.  TRIM:
+// the first part has 16 bits, so that its product with a bf16 number is
+// exact.  limit: a power of two of 8 u to 16 u.
+template <bool TRIM>
+__device__ __forceinline__ void reciprocal(float s, float g, float &ih, float &il, float &limit) {
     const float uh = s * g, ul = fmaf(s, g, -uh);
+    limit = __uint_as_float((__float_as_uint(uh) & 0x7f800000u) + (4u << 23));
     float r = __builtin_amdgcn_rcpf(uh);
     r = fmaf(r, fmaf(-uh, r, 1.f), r);
     ih = TRIM ? __uint_as_float(__float_as_uint(r) & 0xffffff00u) : r;
@@ -85,9 +88,13 @@ template <bool TRIM> __device__ __forceinline__ void reciprocal(float s, float g
 // The two parts are good to 2^-39 of a quotient, of at most 5 where it
 // matters: on a middle the rest is below 2^-36, and what is off a middle is
 // off by at least 2^-33; 2^-35 tells them apart.
-template <bool TRIM> __device__ __forceinline__ float quotient(float x, float ih, float il) {
-    const float ax = fabsf(x);
-    float p = fminf(ax * ih, 16.f), rest;     // the largest code is 6
+// A block whose scale stops at 448 may hold any x: what passes the limit is
+// taken as the limit, a quotient above 8 where the largest code is 6.  (Cut
+// behind the first product instead, x il would still grow with x, and il has
+// either sign.)
+template <bool TRIM> __device__ __forceinline__ float quotient(float x, float ih, float il, float limit) {
+    const float ax = fminf(fabsf(x), limit);
+    float p = ax * ih, rest;
     if constexpr (TRIM) {
         const float p0 = p;                   // exact
         p = fmaf(ax, il, p0);
@@ -143,10 +150,11 @@ __global__ __launch_bounds__(kThreads) void quantize_e2m1_kernel(const SRC *__re
         float q[2][kPer];
         if (g >= 0x1p-80f && g <= 0x1p80f) {
             sc = bad ? 0x7Fu : e4m3_of(__uint_as_float(a), g);
-            float ih, il;
-            reciprocal<kTrim>(e4m3_f(sc), g, ih, il);
+            float ih, il, limit;
+            reciprocal<kTrim>(e4m3_f(sc), g, ih, il, limit);
 #pragma unroll
-            for (int i = 0; i < 2 * kPer; ++i) q[i / kPer][i % kPer] = quotient<kTrim>(f[i / kPer][i % kPer], ih, il);
+            for (int i = 0; i < 2 * kPer; ++i)
+                q[i / kPer][i % kPer] = quotient<kTrim>(f[i / kPer][i % kPer], ih, il, limit);
         } else {
             sc = bad ? 0x7Fu : e4m3_of((double)__uint_as_float(a) / (6.0 * (double)g));
             const double inv = 1.0 / ((double)e4m3_f(sc) * (double)g) * (1.0 + 0x1p-50);
