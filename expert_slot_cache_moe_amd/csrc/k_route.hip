@@ -289,6 +289,9 @@ __global__ __launch_bounds__(kRowsPerBlock *kWave) void route_kernel(
             const float worst = -wave_max_f32(in ? -under : -INFINITY);
             const float next = wave_max_f32(g < G && !in && value > -INFINITY ? over : -INFINITY);
             settled = worst > next || !(next > -INFINITY);
+            // two values of the lowest kind (experts biased out of reach, but
+            // available) add up to -infinity in fp32, not in 64 bits
+            if (top2) settled = settled && __ballot(b > -INFINITY && !(value > -INFINITY)) == 0;
         }
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {

@@ -1,5 +1,7 @@
-"""Borders of the 4-bit rows on the GPU, against the plain 64-bit forms
-(operator_ref.py): codes and scales are equal."""
+"""Borders of the scored router and the 4-bit rows on the GPU, against the
+plain 64-bit forms (operator_ref.py).  Ids, codes and scales are equal;
+routing weights are 64-bit arithmetic rounded once to fp32 (2^-24, and the
+difference of two 64-bit exponentials)."""
 import numpy as np
 import pytest
 import torch
@@ -9,6 +11,8 @@ import operator_ref as ref
 from expert_slot_cache_moe_amd import workloads as W
 
 pytestmark = pytest.mark.gpu
+
+LOW = float(np.finfo(np.float32).min)
 
 
 def _say(*a):
@@ -50,3 +54,32 @@ def test_saturated_e2m1_blocks_take_the_largest_code_and_the_sign(dtype):
     x[:, ::16] = np.minimum(u * 2.0 ** 60, 3e38)[:, None] * g.choice([-1.0, 1.0], (len(globs), 8))
     x = np.clip(x, -3e38, 3e38)
     _check_e2m1(torch.from_numpy(x.astype(np.float32)).to(dtype).cuda(), torch.from_numpy(globs).cuda())
+
+
+# ---------------------------------------------------------------- two-best groups of lowest-value biases
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top_groups,K", [(16, 4, 2, 4), (64, 8, 3, 12), (160, 8, 5, 30), (1024, 16, 4, 64)])
+@pytest.mark.parametrize("open_groups", [0, 1, 2])
+def test_two_best_groups_whose_biases_sum_below_the_lowest_float(score, E, groups, top_groups, K, open_groups):
+    # experts biased by the type's lowest value are available still: their groups fill the choice
+    _say("lowest biases", score, E, groups, top_groups, K, open_groups)
+    g = W.rng(82, "lowest", score, E, open_groups)
+    T, gs = 9, E // groups
+    x = g.standard_normal((T, E)).astype(np.float32)
+    x[1] = 0.5
+    x[2, ::3] = -np.inf
+    for b in (np.full(E, LOW), np.where(g.random(E) < 0.3, LOW / 2, LOW), np.where(np.arange(E) % gs == 0, 0.0, LOW),
+              np.where(np.arange(E) % gs < 2, -LOW, LOW)):
+        b = b.astype(np.float32)
+        b[:open_groups * gs] = 0.0
+        router = m.make_router(score=m.MOE_SCORE_SIGMOID if score == "sigmoid" else m.MOE_SCORE_SOFTMAX,
+                               num_groups=groups, top_groups=top_groups, group_score=m.MOE_GROUP_TOP2,
+                               bias=torch.from_numpy(b).cuda())
+        ids = torch.full((T, K), 77, dtype=torch.int32, device="cuda")
+        w = torch.full((T, K), np.nan, dtype=torch.float32, device="cuda")
+        m.moe_route(router, torch.from_numpy(x).cuda(), K, ids, w)
+        e_ids, e_w = ref.route(x.astype(np.float64), K, score=score, groups=groups, top_groups=top_groups, top2=True,
+                               bias=b.astype(np.float64))
+        assert (ids.cpu().numpy() == e_ids).all()
+        assert (np.abs(_f64(w) - e_w) <= np.abs(e_w) * (2.0 ** -24 + 1e-12) + 2.0 ** -150).all()
