@@ -182,13 +182,15 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // Two products a g rounded once to bf16: the fp32 product rounded first
 // could land on a bf16 middle that it is not on; its error (exact, by fma)
-// then says to which side it belongs.
+// then says to which side it belongs.  Below 2^-126 the error has bits below
+// fp32's last, 2^-149: it is formed 2^64 times as large.
 __device__ __forceinline__ bool on_middle(float p) { return (__float_as_uint(p) & 0xffffu) == 0x8000u; }
 __device__ __forceinline__ float off_middle(float a, float g) {
     const float p = a * g;
     uint32_t u = __float_as_uint(p);
     if (on_middle(p)) {
-        const float err = fmaf(a, g, -p);
+        const float up = fabsf(p) < 1.f ? 0x1p64f : 1.f;
+        const float err = fmaf(a * up, g, -p * up);
         if (err != 0.f) u += ((err > 0.f) == (p > 0.f)) ? 1 : -1;
     }
     return __uint_as_float(u);

@@ -1,7 +1,7 @@
 """Borders of the scored router and the 4-bit rows on the GPU, against the
-plain 64-bit forms (operator_ref.py).  Ids, codes and scales are equal;
-routing weights are 64-bit arithmetic rounded once to fp32 (2^-24, and the
-difference of two 64-bit exponentials)."""
+plain 64-bit forms (operator_ref.py).  Ids, codes, scales and bf16 values are
+equal; routing weights are 64-bit arithmetic rounded once to fp32 (2^-24, and
+the difference of two 64-bit exponentials)."""
 import numpy as np
 import pytest
 import torch
@@ -83,3 +83,34 @@ def test_two_best_groups_whose_biases_sum_below_the_lowest_float(score, E, group
                                bias=b.astype(np.float64))
         assert (ids.cpu().numpy() == e_ids).all()
         assert (np.abs(_f64(w) - e_w) <= np.abs(e_w) * (2.0 ** -24 + 1e-12) + 2.0 ** -150).all()
+
+
+# ---------------------------------------------------------------- E2M1 values below the smallest normal number
+
+def test_subnormal_e2m1_values_are_rounded_once_to_bf16():
+    # products of a code value and a block scale that fp32 rounds onto the middle of two bf16 numbers
+    _say("subnormal values")
+    g = W.rng(83, "subnormal")
+    grid = ref.e4m3_grid()
+    globs, codes, scales = [], [], []
+    for _ in range(4000):
+        s = int(g.integers(1, 24))
+        a = ref.VALUES[1:] * grid[s]
+        # g near an odd multiple of 2^-134 over one of the values: the middles of bf16 below 2^-126
+        v = a[g.integers(0, 7)]
+        globs.append(np.float32((2 * int(g.integers(1, 128)) + 1) * 2.0 ** -134 / v))
+        scales.append(s)
+    globs = np.array(globs, np.float32)
+    globs = np.where(g.random(4000) < 0.5, np.nextafter(globs, np.float32(1)), globs)
+    R = len(globs)
+    c = np.tile(np.arange(16, dtype=np.uint8), (R, 1))
+    packed = torch.from_numpy(c[:, 0::2] | (c[:, 1::2] << 4)).cuda()
+    out = torch.empty((R, 16), dtype=torch.bfloat16, device="cuda")
+    m.moe_dequantize_rows(m.MOE_FMT_E2M1, packed, torch.from_numpy(np.array(scales, np.uint8))[:, None].cuda(), out,
+                          globals=torch.from_numpy(globs).cuda(), rows_per_global=1)
+    val = ref.VALUES[np.arange(16) & 7] * np.where(np.arange(16) & 8, -1.0, 1.0)
+    v = val[None, :] * grid[np.array(scales)][:, None] * globs.astype(np.float64)[:, None]   # exact: at most 33 bits
+    step = np.ldexp(1.0, np.maximum(np.frexp(np.where(v == 0, 1e-300, v))[1] - 8, -133))
+    want = np.rint(v / step) * step                                                          # ties to even
+    bad = _f64(out) != want
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(), _f64(out)[bad][:4], want[bad][:4])
