@@ -22,7 +22,8 @@ def quantized_banks(fmt, w13, w2, hidden, ffn, device="cuda"):
     """The banks of a 4-bit format, uint8 device tensors [E, row_bytes], for
     experts given in bf16: w13 [E, 2F*H] and w2 [E, H*F] as uint8, int16 or
     bfloat16 rows (numpy or torch).  E2M1 global scales are the matrix's
-    largest magnitude / (6 * 448), or 1 for a matrix of zeros."""
+    largest finite magnitude / (6 * 448), or 1 for a matrix of zeros; a block
+    with NaN or infinity is NaN, the others keep their values."""
     banks = []
     for w, n, k in ((w13, 2 * ffn, hidden), (w2, hidden, ffn)):
         t = torch.from_numpy(np.ascontiguousarray(w)) if isinstance(w, np.ndarray) else w
@@ -30,7 +31,7 @@ def quantized_banks(fmt, w13, w2, hidden, ffn, device="cuda"):
         t = t.to(device).contiguous().view(torch.uint8).view(torch.bfloat16).view(E * n, k)
         glob = None
         if fmt == MOE_FMT_E2M1:
-            amax = t.abs().amax(1).float().view(E, n).amax(1) / (6 * 448)
+            amax = t.abs().nan_to_num_(nan=0.0, posinf=0.0).amax(1).float().view(E, n).amax(1) / (6 * 448)
             glob = torch.where(amax > 0, amax, torch.ones_like(amax))
         blk = 16 if fmt == MOE_FMT_E2M1 else 32
         codes = torch.empty((E * n, k // 2), dtype=torch.uint8, device=device)

@@ -1,7 +1,7 @@
-"""Borders of the scored router and the 4-bit rows on the GPU, against the
-plain 64-bit forms (operator_ref.py).  Ids, codes, scales and bf16 values are
-equal; routing weights are 64-bit arithmetic rounded once to fp32 (2^-24, and
-the difference of two 64-bit exponentials)."""
+"""Borders of the scored router, the 4-bit rows and the layer's 4-bit banks
+on the GPU, against the plain 64-bit forms (operator_ref.py).  Ids, codes,
+scales and bf16 values are equal; routing weights are 64-bit arithmetic
+rounded once to fp32 (2^-24, and the difference of two 64-bit exponentials)."""
 import numpy as np
 import pytest
 import torch
@@ -114,3 +114,33 @@ def test_subnormal_e2m1_values_are_rounded_once_to_bf16():
     want = np.rint(v / step) * step                                                          # ties to even
     bad = _f64(out) != want
     assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(), _f64(out)[bad][:4], want[bad][:4])
+
+
+# ---------------------------------------------------------------- 4-bit banks of experts that are not finite
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "e2m1"])
+def test_quantized_banks_keep_the_finite_blocks_beside_nan_and_infinity(fmt):
+    from expert_slot_cache_moe_amd.layer import quantized_banks
+
+    _say("banks", fmt)
+    code = m.MOE_FMT_MXFP4 if fmt == "mxfp4" else m.MOE_FMT_E2M1
+    E, H, F = 4, 64, 96
+    g = W.rng(84, "banks", fmt)
+    w13, w2 = W.bf16_expert_rows(g, E, H, F)
+    w2.view(np.uint16)[1, 7] = 0x7F80             # +infinity
+    w2.view(np.uint16)[2, 100] = 0x7FC0           # NaN
+    w13.view(np.uint16)[0, 5] = 0xFF80            # -infinity
+    w13.view(np.uint16)[3] = 0x7F80               # nothing else
+    banks = [b.cpu().numpy() for b in quantized_banks(code, w13, w2, H, F)]
+    per = 3 if fmt == "e2m1" else 2
+    for i, (raw, n, k) in enumerate(((w13, 2 * F, H), (w2, H, F))):
+        x = ref.bf16_f64(raw.view(np.uint16)).reshape(E * n, k)
+        glob = None
+        if fmt == "e2m1":
+            glob = banks[per * i + 2].reshape(-1).view(np.float32)
+            amax = np.where(np.isfinite(x), np.abs(x), 0.0).reshape(E, -1).max(1)
+            assert np.allclose(glob, np.where(amax > 0, amax / 2688, 1.0), rtol=1e-6)
+        codes, scales, vals = ref.quantize(x, fmt, glob, n)
+        assert (banks[per * i].reshape(E * n, -1) == codes).all()
+        assert (banks[per * i + 1].reshape(E * n, -1) == scales).all()
+        assert np.isfinite(vals).any(1).reshape(E, n).all(1).sum() == E - (i == 0)
