@@ -97,7 +97,8 @@ moe_status_t check_mx_sizes(int32_t P, int32_t n, int32_t k, int32_t T, int32_t 
 }
 
 moe_status_t check_routed_mx_sizes(int32_t P, int32_t H, int32_t F, int32_t T, int32_t K) {
-    if (H < 1 || F < 1 || F > kMxMaxN / 2) return fail(MOE_INVALID_ARG, "hidden %d / ffn %d", H, F);
+    if (H < 1 || F < 1) return fail(MOE_INVALID_ARG, "hidden %d / ffn %d", H, F);
+    if (F > kMxMaxN / 2) return fail(MOE_UNSUPPORTED, "ffn %d > %d", F, kMxMaxN / 2);
     if (H % 32 || F % 32) return fail(MOE_UNSUPPORTED, "hidden %d / ffn %d are not multiples of 32", H, F);
     if (T > 65535) return fail(MOE_UNSUPPORTED, "T=%d > 65535", T);
     moe_status_t st = check_mx_sizes(P, 2 * F, H, T, K);

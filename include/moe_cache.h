@@ -491,7 +491,8 @@ moe_status_t moe_layer_decode_router(moe_cache_t *cache, int32_t layer, const vo
  * Asynchronous, capturable.  Errors: MOE_INVALID_ARG (another format or
  * type, rows < 0, cols < 1 or not a multiple of B, a stride below cols,
  * rows_per_global < 1 with globals, null or misaligned pointers: src to
- * its element, codes to 8 bytes (MXFP4: 16), globals to 4). */
+ * its element, codes to 8 bytes (MXFP4: 16), globals to 4),
+ * MOE_UNSUPPORTED (rows > 2^32, cols > 2^19). */
 moe_status_t moe_quantize_rows(int32_t weight_format, int32_t src_type, const void *src_dev,
                                int64_t src_stride, int64_t rows, int32_t cols,
                                const float *globals_dev, int64_t rows_per_global, void *codes_dev,
@@ -553,7 +554,8 @@ int64_t moe_routed_mx_workspace_bytes(int32_t num_rows, int32_t hidden, int32_t 
  * Results differ from moe_routed_decode's by the quantisation of x and of
  * the activation.  Arguments as moe_routed_decode, x 16-byte aligned.
  * Errors: as moe_mx_product; MOE_INVALID_ARG for another format;
- * MOE_UNSUPPORTED (hidden or ffn not a multiple of 32, T > 65535). */
+ * MOE_UNSUPPORTED (hidden or ffn not a multiple of 32, hidden or ffn >
+ * 2^16, T > 65535). */
 moe_status_t moe_routed_decode_mx(const moe_pool_t *pool, const void *x_dev, const int32_t *idx_dev,
                                   const float *w_dev, int32_t T, int32_t K, const float *addend_dev,
                                   void *out_dev, void *workspace_dev, int64_t workspace_bytes,
