@@ -91,9 +91,10 @@ __device__ __forceinline__ void reciprocal(float s, float g, float &ih, float &i
 // A block whose scale stops at 448 may hold any x: what passes the limit is
 // taken as the limit, a quotient above 8 where the largest code is 6.  (Cut
 // behind the first product instead, x il would still grow with x, and il has
-// either sign.)
+// either sign.)  The median, as fminf would first quiet a NaN in an
+// instruction of its own.
 template <bool TRIM> __device__ __forceinline__ float quotient(float x, float ih, float il, float limit) {
-    const float ax = fminf(fabsf(x), limit);
+    const float ax = __builtin_amdgcn_fmed3f(fabsf(x), 0.f, limit);
     float p = ax * ih, rest;
     if constexpr (TRIM) {
         const float p0 = p;                   // exact
@@ -181,17 +182,16 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // Two products a g rounded once to bf16: the fp32 product rounded first
-// could land on a bf16 middle that it is not on; its error (exact, by fma)
-// then says to which side it belongs.  Below 2^-126 the error has bits below
-// fp32's last, 2^-149: it is formed 2^64 times as large.
+// could land on a bf16 middle that it is not on; its error (in 64 bits: of a
+// product below 2^-126 it has bits under fp32's last) then says to which side
+// it belongs.
 __device__ __forceinline__ bool on_middle(float p) { return (__float_as_uint(p) & 0xffffu) == 0x8000u; }
 __device__ __forceinline__ float off_middle(float a, float g) {
     const float p = a * g;
     uint32_t u = __float_as_uint(p);
     if (on_middle(p)) {
-        const float up = fabsf(p) < 1.f ? 0x1p64f : 1.f;
-        const float err = fmaf(a * up, g, -p * up);
-        if (err != 0.f) u += ((err > 0.f) == (p > 0.f)) ? 1 : -1;
+        const double err = (double)a * (double)g - (double)p;
+        if (err != 0.0) u += ((err > 0.0) == (p > 0.f)) ? 1 : -1;
     }
     return __uint_as_float(u);
 }
