@@ -108,7 +108,8 @@ template <bool TRIM> __device__ __forceinline__ float quotient(float x, float ih
     const uint32_t u = __float_as_uint(p);
     const uint32_t odd = (u + (uint32_t)((int)__float_as_uint(rest) >> 31)) | 1u;
     const uint32_t v = fabsf(rest) > 0x1p-35f ? odd : u;
-    return __uint_as_float(v | (__float_as_uint(x) & 0x80000000u));
+    // (x ih may vanish and leave p the sign of x il)
+    return copysignf(__uint_as_float(v), x);
 }
 
 // MXFP4: eight elements a lane.

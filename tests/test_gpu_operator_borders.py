@@ -56,6 +56,18 @@ def test_saturated_e2m1_blocks_take_the_largest_code_and_the_sign(dtype):
     _check_e2m1(torch.from_numpy(x.astype(np.float32)).to(dtype).cuda(), torch.from_numpy(globs).cuda())
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_e2m1_quotients_below_the_smallest_float_are_zeros_of_the_sign(dtype):
+    # blocks of one large value beside values down to the smallest: x / (s g) of 2^-149 and less
+    _say("vanishing quotients", dtype)
+    g = W.rng(85, "vanishing", str(dtype))
+    R, C = 6000, 64
+    globs = ((g.random(R) + 1) * 2.0 ** g.integers(20, 80, R)).astype(np.float32)
+    x = (g.random((R, C)) + 1) * 2.0 ** g.integers(-133, -60, (R, C)) * g.choice([-1.0, 1.0], (R, C))
+    x[:, ::16] = np.minimum(6 * globs[:, None].astype(np.float64) * 2.0 ** g.integers(-8, 9, (R, C // 16)), 3e38)
+    _check_e2m1(torch.from_numpy(x.astype(np.float32)).to(dtype).cuda(), torch.from_numpy(globs).cuda())
+
+
 # ---------------------------------------------------------------- two-best groups of lowest-value biases
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
