@@ -132,7 +132,10 @@ __device__ __forceinline__ int place(int32_t *cnt, int row) {
 // Block 0 makes the lists; the others, if any, quantise x, so the one goes on
 // beside the other.  lists = 0: every block quantises.  staged: the sorted
 // ids are put together in LDS and written in order (a scattered store of 64
-// lanes takes 64 turns: 24576 ids 24 -> 12 us), where they fit.
+// lanes takes 64 turns: 24576 ids 24 -> 12 us), where they fit: up to some
+// 36000.  One block makes all lists, so their time grows with the ids and
+// steps up there (a product over 256 matrices of 256 x 256, a call: 32768
+// ids 32 us, 36000 36, 37600 47, 65536 72, 131072 131).
 struct PrepareParams {
     const int32_t *idx;
     int32_t R, P, run_length, lists, staged;
@@ -750,7 +753,11 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // The scales of two stages (16 blocks) of a row, from block b0; past the
 // row's last block 0.  VEC: 16, rows are whole aligned 16-byte vectors; 4,
-// whole dwords; 1, neither.
+// whole dwords; 1, neither: a load for each byte, and at 128 and 256 routes
+// more registers than there are (76 to 108 bytes a lane in scratch), which
+// costs up to half of the rate (k 2944 / 2880, us: 256 matrices of 2048 rows
+// for 96 routes each 267 / 517, for 12 each 186 / 255; one 4096 x k for 8192
+// rows 100 / 203).
 template <int VEC>
 __device__ __forceinline__ u32x4 load_scales(const uint8_t *row, int b0, int nblk) {
     u32x4 v;
@@ -1069,7 +1076,8 @@ namespace {
 // Blocks of the many-block form that keep the device busy; with fewer, k is
 // split over the waves instead (split / many, us: 64 blocks 4.7 / 9.1, 256
 // 11.3 / 10.7, 320 8.4 / 9.9, 384 27.5 / 32.0, 512 19.6 / 15.2 and 24.9 /
-// 16.4, 1024 33.9 / 33.0).
+// 16.4, 1024 33.9 / 33.0).  A coarse rule: between 64 and 512 the two cross
+// more than once, as k and the lists decide too; the worst of these costs 6 %.
 constexpr int64_t kManyBlocks = 512;
 // Blocks for the passes over one matrix row's list, where lists may be long:
 // the longest list of a skewed batch is the kernel's last block.  1200 routes

@@ -14,9 +14,9 @@
 // scale itself, a / (6 g) against the middles of E4M3.
 //
 // Bound by memory: a 134M element bf16 matrix (340 MB of both sides) to
-// MXFP4 takes 70 us on MI355X, back 62 us (4.9 and 5.4 TB/s; a large copy
-// reaches 4.9); to E2M1 78 us, bound by the quotients, back 74 us.  One row
-// of 2048 takes 1.4 us either way, less than its launch.
+// MXFP4 and back takes 133 us on MI355X (5.1 TB/s; a large copy reaches
+// 4.9); to E2M1 and back 144, the way there 78 to 82 of them, bound by the
+// quotients.  One row of 2048 takes 1.4 us either way, less than its launch.
 #include "k_rows.inc"
 
 namespace moe {

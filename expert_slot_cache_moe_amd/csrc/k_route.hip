@@ -17,11 +17,13 @@
 //
 // On MI355X one row of 256 grouped experts takes 4.8 us, the latency of its
 // steps one behind the other; 16384 rows of 512 (33.5 MB) 22 us, where
-// reading them takes 7: bound by the instructions of a row (exponentials, ballots and the 64-bit
-// ranks of a dozen candidates), of which the waves of a SIMD issue one a
-// cycle.  The long way for every row took 95.  Four rows to a wave, whose
-// serial parts overlap but whose registers allow fewer waves, took 21.3 at
-// 512 experts and 12.2 (one row: 10.8) at 256.
+// reading them takes 7.  What a row waits for shows in the built code: each
+// of its eight values loads its bias on a branch and waits for it there, and
+// the kind of score, the bias and the groups are branches of every value;
+// what of the 22 us each part costs has not been counted.  The long way for
+// every row took 95.  Four rows to a wave, whose serial parts overlap but
+// whose registers allow fewer waves, took 21.3 at 512 experts and 12.2 (one
+// row: 10.8) at 256.
 #include "moe_internal.h"
 
 namespace moe {

@@ -40,7 +40,10 @@ moe_status_t layer_decode(moe_cache_t *c, int32_t layer, const void *x, const fl
     const bool timing = c->timing != 0;
     hipEvent_t *tev = timing ? &c->tev[(size_t)layer * 6] : nullptr;
 
-    // Few token rows: the top-k runs inside the admission kernel.
+    // Few token rows: the top-k runs inside the admission kernel.  A router's
+    // routes take a launch of their own (one token, top 8 of 256 experts of
+    // 512 x 2048, all resident, captured: 37.6 us a step, with a softmax router
+    // 40.4, with a sigmoid router of 8 groups and a bias 42.6).
     const bool fused_topk = !router && T <= kFusedTopkRows &&
                             admit_fused_topk_supported(c->d.num_experts, c->d.num_slots, K);
     auto pick_routes = [&]() {

@@ -110,6 +110,9 @@ class SlotCacheLayers:
 
     def decode_hybrid(self, layer, x, logits, K, out, ids_out=None, w_out=None, max_fetch=-1,
                       stream=None):
+        """decode with the misses on host threads; not with routers, whichever
+        layer they are for (a layer without one can be stepped through
+        moe_layer_decode_hybrid itself)."""
         if any(r is not None for r in self.routers):
             raise ValueError("the hybrid step routes by softmax top-k; it takes no router")
         sh = self._shared(layer)
