@@ -21,6 +21,7 @@ MOE_FMT_BF16, MOE_FMT_E2M1, MOE_FMT_MXFP4 = 0, 1, 2
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
 MOE_TYPE_F32, MOE_TYPE_BF16 = 0, 1
+MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_SWIGLU = range(4)
 MOE_MAX_BANKS = 6
 MOE_NUM_STATS = 8
 STAT_NAMES = ("calls", "met", "missed", "overflow", "invalid", "pf_calls", "pf_filled",
@@ -73,6 +74,13 @@ class moe_mx_bank_t(C.Structure):
     _fields_ = [
         ("num_rows", C.c_int32), ("n", C.c_int32), ("k", C.c_int32), ("codes_dev", C.c_void_p),
         ("scales_dev", C.c_void_p),
+    ]
+
+
+class moe_bank_t(C.Structure):
+    _fields_ = [
+        ("weight_format", C.c_int32), ("num_rows", C.c_int32), ("n", C.c_int32), ("k", C.c_int32),
+        ("weights_dev", C.c_void_p), ("scales_dev", C.c_void_p), ("globals_dev", C.c_void_p),
     ]
 
 
@@ -129,6 +137,13 @@ def lib():
             "moe_mx_product": (st, [P, P, i64, P, i32, i32, i32, i32, P, P, i64, P]),
             "moe_routed_mx_workspace_bytes": (i64, [i32, i32, i32, i32, i32]),
             "moe_routed_decode_mx": (st, [P, P, P, P, i32, i32, P, P, P, i64, P]),
+            "moe_group_routes_workspace_bytes": (i64, [i32, i32, i32]),
+            "moe_group_routes": (st, [P, i32, i32, i32, P, P, P, i64, P]),
+            "moe_grouped_product": (st, [P, P, i64, i32, P, i32, P, P, i32, P, i32, i32, i32, P, i32, P, i64,
+                                         i32, P]),
+            "moe_linear": (st, [P, P, i64, i32, i32, i32, P, i32, P, i64, i32, P, i64, P]),
+            "moe_routed_prefill_workspace_bytes": (i64, [i32, i32, i32, i32, i32, i32]),
+            "moe_routed_prefill": (st, [P, P, P, P, i32, i32, P, P, P, i64, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -620,6 +635,152 @@ def moe_routed_decode_mx(pool: moe_pool_t, x, idx, w, out, workspace, addend=Non
     if addend is not None:
         _want(addend, "addend", (T, pool.hidden), _F32)
     _check(lib().moe_routed_decode_mx(
+        C.byref(pool), _dev_ptr(x), _dev_ptr(idx), _dev_ptr(w), T, K, _dev_ptr(addend), _dev_ptr(out),
+        _dev_ptr(workspace), workspace.nbytes, _stream_on(dev, stream)))
+
+
+# ---------------------------------------------------------------- grouped and dense products
+
+def make_bank(fmt: int, weights, scales=None, globals=None) -> moe_bank_t:
+    """Matrices of a weight format, contiguous device tensors: bf16 weights
+    [num_rows, n, k]; or uint8 codes [num_rows, n, k/2] and scales [num_rows,
+    n, k/16 (E2M1) or k/32 (MXFP4)], for E2M1 with globals float32 [num_rows]
+    or None."""
+    if weights.dim() != 3:
+        raise ValueError("weights: expected [num_rows, n, k] (4-bit codes: k/2)")
+    P, n, w = weights.shape
+    _on_current_device(weights, scales, globals)
+    b = moe_bank_t()
+    b.weight_format, b.num_rows, b.n = fmt, P, n
+    if fmt == MOE_FMT_BF16:
+        if _type_of(weights, "weights") != MOE_TYPE_BF16:
+            raise ValueError("weights must be bfloat16")
+        _want(weights, "weights", (P, n, w))
+        if scales is not None or globals is not None:
+            raise ValueError("bf16 matrices have no scales")
+        b.k = w
+    else:
+        b.k = 2 * w
+        _want(weights, "weights", (P, n, w), _U8)
+        if scales is None:
+            raise ValueError("4-bit matrices need scales")
+        _want(scales, "scales", (P, n, b.k // (16 if fmt == MOE_FMT_E2M1 else 32)), _U8)
+        if globals is not None:
+            _want(globals, "globals", (P,), _F32)
+        b.scales_dev, b.globals_dev = _dev_ptr(scales), _dev_ptr(globals)
+    b.weights_dev = _dev_ptr(weights)
+    b._keep = tuple(t for t in (weights, scales, globals) if t is not None)
+    b._device = weights.get_device()
+    return b
+
+
+def moe_group_routes_workspace_bytes(num_rows: int, T: int, K: int) -> int:
+    return int(lib().moe_group_routes_workspace_bytes(num_rows, T, K))
+
+
+def moe_group_routes(idx, num_rows: int, offsets, order, workspace=None, stream=None) -> None:
+    """idx int32 [T, K] -> offsets int32 [num_rows + 1], order int32 [T * K];
+    workspace may be None where moe_group_routes_workspace_bytes is 0."""
+    if idx.dim() != 2:
+        raise ValueError("idx: expected [T, K]")
+    T, K = idx.shape
+    dev = _on_current_device(idx, offsets, order, workspace)
+    _want(idx, "idx", (T, K), _I32)
+    _want(offsets, "offsets", (num_rows + 1,), _I32)
+    _want(order, "order", (T * K,), _I32)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _check(lib().moe_group_routes(
+        idx.data_ptr(), T, K, num_rows, offsets.data_ptr(), order.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+        _stream_on(dev, stream)))
+
+
+def _product_rows(bank, x, out, activation, bias, bias_shape, dev):
+    """(rows of x, their stride, rows of out, their stride, bias type, out type)."""
+    x_rows, k, x_stride = _rows_of(x, "x")
+    if k != bank.k:
+        raise ValueError(f"x has {k} columns, the bank's matrices {bank.k}")
+    if _type_of(x, "x") != MOE_TYPE_BF16:
+        raise ValueError("x must be bfloat16")
+    out_rows, cols, out_stride = _rows_of(out, "out")
+    if cols != (bank.n // 2 if activation == MOE_ACT_SWIGLU else bank.n):
+        raise ValueError(f"out has {cols} columns for matrices of {bank.n} rows")
+    if getattr(bank, "_device", None) != dev:
+        _on_current_device(*getattr(bank, "_keep", ()))
+        bank._device = dev
+    bias_type = 0
+    if bias is not None:
+        _want(bias, "bias", bias_shape)
+        bias_type = _type_of(bias, "bias")
+    return x_rows, x_stride, out_rows, out_stride, bias_type, _type_of(out, "out")
+
+
+def _indices(t, what, n):
+    if t is None:
+        return None
+    _want(t, what, (n,), _I32)
+    return t.data_ptr()
+
+
+def moe_grouped_product(bank: moe_bank_t, x, offsets, out, matrices=None, gather=None, gather_div: int = 1,
+                        scatter=None, activation: int = MOE_ACT_NONE, bias=None, stream=None) -> None:
+    """x [rows, k] bfloat16, out [rows, n or n/2] float32 or bfloat16 (both may
+    be strided), offsets int32 [G + 1], matrices int32 [G]; gather and scatter
+    int32 [R], where R is their length, or the rows of x without gather and
+    scatter; bias [num_rows, n]."""
+    dev = _on_current_device(x, offsets, out, matrices, gather, scatter, bias)
+    x_rows, x_stride, out_rows, out_stride, bias_type, out_type = _product_rows(
+        bank, x, out, activation, bias, (bank.num_rows, bank.n), dev)
+    R = x_rows if gather is None and scatter is None else (gather if gather is not None else scatter).numel()
+    G = offsets.numel() - 1
+    _check(lib().moe_grouped_product(
+        C.byref(bank), x.data_ptr(), x_stride, x_rows, _indices(offsets, "offsets", G + 1), G,
+        _indices(matrices, "matrices", G), _indices(gather, "gather", R), gather_div,
+        _indices(scatter, "scatter", R), R, activation, bias_type, None if bias is None else bias.data_ptr(),
+        out_type, out.data_ptr(), out_stride, out_rows, _stream_on(dev, stream)))
+
+
+def moe_linear(bank: moe_bank_t, x, out, activation: int = MOE_ACT_NONE, bias=None, residual=None,
+               stream=None) -> None:
+    """out = act(x W^T + bias) + residual: x [T, k] bfloat16, out [T, n or
+    n/2] float32 or bfloat16, bias [n], residual shaped as out (it may be out);
+    rows of x, out and residual may be strided."""
+    dev = _on_current_device(x, out, bias, residual)
+    T, x_stride, out_rows, out_stride, bias_type, out_type = _product_rows(
+        bank, x, out, activation, bias, (bank.n,), dev)
+    if out_rows != T:
+        raise ValueError(f"out has {out_rows} rows for {T} of x")
+    res, res_type, res_stride = None, 0, 0
+    if residual is not None:
+        if residual.shape != out.shape:
+            raise ValueError(f"residual: expected the shape of out {tuple(out.shape)}, got {tuple(residual.shape)}")
+        res, res_type, res_stride = residual.data_ptr(), _type_of(residual, "residual"), \
+            _rows_of(residual, "residual")[2]
+    _check(lib().moe_linear(
+        C.byref(bank), x.data_ptr(), x_stride, T, activation, bias_type,
+        None if bias is None else bias.data_ptr(), res_type, res, res_stride, out_type, out.data_ptr(),
+        out_stride, _stream_on(dev, stream)))
+
+
+def moe_routed_prefill_workspace_bytes(weight_format: int, num_rows: int, hidden: int, ffn: int, T: int,
+                                       K: int) -> int:
+    return int(lib().moe_routed_prefill_workspace_bytes(weight_format, num_rows, hidden, ffn, T, K))
+
+
+def moe_routed_prefill(pool: moe_pool_t, x, idx, w, out, workspace, addend=None, stream=None) -> None:
+    """moe_routed_decode for prompts of up to 2^22 routes."""
+    T, K = idx.shape
+    dev = _on_current_device(x, idx, w, out, workspace, addend)
+    if _type_of(x, "x") != MOE_TYPE_BF16 or _type_of(out, "out") != MOE_TYPE_BF16:
+        raise ValueError("x and out must be bfloat16")
+    _want(x, "x", (T, pool.hidden))
+    _want(idx, "idx", (T, K), _I32)
+    _want(w, "w", (T, K), _F32)
+    _want(out, "out", (T, pool.hidden))
+    if addend is not None:
+        _want(addend, "addend", (T, pool.hidden), _F32)
+    _check(lib().moe_routed_prefill(
         C.byref(pool), _dev_ptr(x), _dev_ptr(idx), _dev_ptr(w), T, K, _dev_ptr(addend), _dev_ptr(out),
         _dev_ptr(workspace), workspace.nbytes, _stream_on(dev, stream)))
 

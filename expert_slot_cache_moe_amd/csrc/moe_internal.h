@@ -381,6 +381,44 @@ bool mx_launchable(const MxParams &p);
 // and K split, takes a first one's lists where it wants runs of that length.
 hipError_t launch_mx_product(const MxParams &p, int *list_length, hipStream_t s);
 
+// Lists of routes by row (k_lists.hip).
+constexpr int kListsMaxRows = 32768, kListsMaxRoutes = 1 << 22;
+size_t lists_workspace_bytes(int P, int64_t R);
+hipError_t launch_lists(const int32_t *idx, int R, int P, int32_t *offsets, int32_t *order, int32_t *counts,
+                        hipStream_t s);
+
+// Products of bf16 rows with matrices in any weight format, grouped by
+// matrix (k_product.hip).
+struct ProductParams {
+    const uint8_t *w, *scales;       // bf16 [P][n][k], or codes [P][n][k/2] and scales
+    const float *globals;            // E2M1: [P]
+    int32_t fmt, P, n, k;
+    const uint16_t *x;               // bf16 [x_rows], x_stride apart
+    int64_t x_stride;
+    int32_t x_rows;
+    const int32_t *offsets;          // [G + 1], or NULL: one group of all R places
+    const int32_t *matrices;         // [G], or NULL: group g takes matrix g
+    int32_t G, R;
+    const int32_t *gather;           // [R], or NULL: place i reads row i / gather_div
+    int32_t gather_div;
+    const int32_t *scatter;          // [R], or NULL: place i writes row i
+    int32_t out_rows;
+    int32_t act;
+    const void *bias;                // [P][n] or NULL
+    int32_t bias_type;
+    const void *residual;            // [out_rows][cols] or NULL
+    int32_t res_type;
+    int64_t res_stride;
+    void *out;
+    int32_t out_type;
+    int64_t out_stride;
+};
+constexpr int kProductMaxMatrices = 32768, kProductMaxN = 1 << 20, kProductMaxK = 1 << 16,
+              kProductMaxPlaces = 1 << 22;
+// false: a grid's threads would pass the 32 bits that count them.
+bool product_launchable(const ProductParams &p);
+hipError_t launch_product(const ProductParams &p, hipStream_t s);
+
 // The single-token layer step in two launches: stage 1 = miss gather
 // (+ the fetched experts' gate/up dots into gu [plan][2F]) | shared gate/up
 // | resident routes' gate/up; stage 2 = all down projections + combine.

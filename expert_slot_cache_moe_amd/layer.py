@@ -9,7 +9,9 @@ import torch
 
 from . import (MOE_FMT_BF16, MOE_FMT_E2M1, make_pool, make_shared, moe_bank_row_bytes,
                moe_cache_create, moe_cache_destroy, moe_layer_decode, moe_layer_decode_hybrid,
-               moe_layer_decode_router, moe_quantize_rows)
+               moe_layer_decode_router, moe_quantize_rows, moe_route, moe_routed_prefill,
+               moe_routed_prefill_workspace_bytes, moe_routed_workspace_bytes, moe_shared_expert,
+               moe_topk)
 
 
 def pinned(a: np.ndarray) -> torch.Tensor:
@@ -118,6 +120,30 @@ class SlotCacheLayers:
         sh = self._shared(layer)
         moe_layer_decode_hybrid(self.cache, layer, x, logits, K, out, shared=sh, max_fetch=max_fetch,
                                 ids_out=ids_out, w_out=w_out, stream=stream)
+
+    def prefill(self, layer, x, logits, K, out, ids_out=None, w_out=None, pool=None):
+        """A prompt's rows through all of the layer's experts, on the current
+        stream: the routes of decode(), the shared expert, and
+        moe_routed_prefill over `pool` (streamed_pool(layer), copied here if
+        not given).  The cache and its statistics stay as they are; any number
+        of tokens up to 65535."""
+        T = x.shape[0]
+        ids = torch.empty((T, K), dtype=torch.int32, device=self.device) if ids_out is None else ids_out
+        w = torch.empty((T, K), dtype=torch.float32, device=self.device) if w_out is None else w_out
+        if self.routers[layer] is None:
+            moe_topk(logits, K, ids, w)
+        else:
+            moe_route(self.routers[layer], logits, K, ids, w)
+        shared, addend = self._shared(layer), None
+        if shared is not None:
+            addend = torch.empty((T, self.H), dtype=torch.float32, device=self.device)
+            n = moe_routed_workspace_bytes(MOE_FMT_BF16, self.H, shared.ffn, T, 1)
+            moe_shared_expert(shared, self.H, x, addend, torch.empty(n, dtype=torch.uint8, device=self.device))
+        if pool is None:
+            pool = self.streamed_pool(layer)
+        n = moe_routed_prefill_workspace_bytes(self.fmt, pool.num_rows, self.H, self.F, T, K)
+        moe_routed_prefill(pool, x, ids, w, out, torch.empty(n, dtype=torch.uint8, device=self.device),
+                           addend=addend)
 
     def streamed_pool(self, layer):
         """The whole layer's experts copied to device memory, rows = expert

@@ -561,6 +561,110 @@ moe_status_t moe_routed_decode_mx(const moe_pool_t *pool, const void *x_dev, con
                                   void *out_dev, void *workspace_dev, int64_t workspace_bytes,
                                   void *stream);
 
+/* ---------------------------------------------------------------- grouped and dense products */
+
+/* Matrices [n][k] of a pool bank in any weight format. */
+typedef struct {
+    int32_t weight_format;    /* MOE_FMT_*                                      */
+    int32_t num_rows;         /* matrices, 1..32768                             */
+    int32_t n, k;             /* k: any for bf16, a multiple of 32 for 4 bits   */
+    const void *weights_dev;  /* bf16 [num_rows][n][k]; or codes [num_rows][n][k/2],
+                                 16-byte aligned                                */
+    const void *scales_dev;   /* E2M1: E4M3 [num_rows][n][k/16], 2-byte aligned;
+                                 MXFP4: E8M0 [num_rows][n][k/32]; bf16: unused  */
+    const float *globals_dev; /* E2M1: fp32 [num_rows], or NULL for 1           */
+} moe_bank_t;
+
+/* What is done to a product's sums. */
+enum {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_SILU = 1,         /* y / (1 + exp(-y))                              */
+    MOE_ACT_GELU = 2,         /* y (1 + erf(y / sqrt(2))) / 2                   */
+    MOE_ACT_SWIGLU = 3        /* silu(y[:n/2]) * y[n/2:], n even: n/2 columns   */
+};
+
+/* Bytes of device workspace moe_group_routes needs (0 for short lists, and
+ * for sizes it refuses). */
+int64_t moe_group_routes_workspace_bytes(int32_t num_rows, int32_t T, int32_t K);
+
+/* Routes sorted by the matrix row they name.  idx_dev: int32 [T][K].
+ * order_dev: int32 [T K], the route numbers t K + j by row, ascending within a
+ * row, those whose id is outside [0, num_rows) last; offsets_dev: int32
+ * [num_rows + 1], where each row's routes begin, and where those without a row
+ * do.  workspace_dev: moe_group_routes_workspace_bytes(...), 4-byte aligned;
+ * calls that share it must be ordered.  Asynchronous, capturable.  Errors:
+ * MOE_INVALID_ARG (sizes, null or misaligned pointers, workspace too small),
+ * MOE_UNSUPPORTED (num_rows > 32768, T K > 2^22). */
+moe_status_t moe_group_routes(const int32_t *idx_dev, int32_t T, int32_t K, int32_t num_rows,
+                              int32_t *offsets_dev, int32_t *order_dev, void *workspace_dev,
+                              int64_t workspace_bytes, void *stream);
+
+/* Rows of bf16 times matrices, the rows lying side by side by matrix.  There
+ * are R places; group g of num_groups holds places [offsets[g], offsets[g + 1])
+ * and takes matrix m = matrices[g] (matrices_dev NULL: m = g):
+ *   y = W_m x[in(i)] + bias_m,   out[out(i)] = act(y)
+ * with in(i) = gather[i] / gather_div, or i without gather, and out(i) =
+ * scatter[i], or i without scatter.  With the lists of moe_group_routes a
+ * gate/up product gathers (gather = order, gather_div = K) and a down product
+ * scatters (scatter = order).
+ *  - Sums, bias and activation are fp32, rounded once to out_type; 4-bit
+ *    weights are multiplied at their exact values (an E2M1 matrix's global
+ *    scale multiplies the sum), a NaN scale makes the outputs it reaches NaN.
+ *  - A group whose matrix is outside [0, num_rows) gets rows of zeros.
+ *  - Places in no group, places whose row of x is outside [0, x_rows) and
+ *    places whose row of out is outside [0, out_rows) are left out: nothing is
+ *    written for them.  Rows of out that no place names stay as they were.
+ *  - offsets ascend from at least 0 to at most R (others are cut to that
+ *    range); two places must not name one row of out.
+ * Within a call a place's result depends on its matrix's bytes and its x
+ * alone; calls of other sizes may add in another order.
+ * x_dev: bf16 [x_rows] rows, x_stride elements apart; bias_dev: [num_rows][n]
+ * of bias_type, or NULL; out_dev: [out_rows] rows of n (SWIGLU: n/2) of
+ * out_type, out_stride elements apart, the gaps not written; offsets_dev:
+ * int32 [num_groups + 1]; matrices_dev: int32 [num_groups]; gather_dev,
+ * scatter_dev: int32 [R].  Asynchronous, capturable.  Errors: MOE_INVALID_ARG
+ * (bank, sizes, strides, types, activation, null or misaligned pointers;
+ * without gather x_rows < R; without scatter out_rows < R; matrices NULL with
+ * more groups than matrices), MOE_UNSUPPORTED (num_rows or num_groups > 32768,
+ * R > 2^22, n > 2^20, k > 2^16, or so many tiles that a launch would have 2^32
+ * threads). */
+moe_status_t moe_grouped_product(const moe_bank_t *bank, const void *x_dev, int64_t x_stride,
+                                 int32_t x_rows, const int32_t *offsets_dev, int32_t num_groups,
+                                 const int32_t *matrices_dev, const int32_t *gather_dev,
+                                 int32_t gather_div, const int32_t *scatter_dev, int32_t R,
+                                 int32_t activation, int32_t bias_type, const void *bias_dev,
+                                 int32_t out_type, void *out_dev, int64_t out_stride, int32_t out_rows,
+                                 void *stream);
+
+/* T rows of bf16 times one matrix (a bank of num_rows = 1):
+ *   out[t] = act(W x_t + bias) + residual[t].
+ * residual_dev: [T] rows of out's columns, of residual_type,
+ * residual_stride elements apart, or NULL; it may be out itself (same type and
+ * stride).  Everything else as moe_grouped_product. */
+moe_status_t moe_linear(const moe_bank_t *bank, const void *x_dev, int64_t x_stride, int32_t T,
+                        int32_t activation, int32_t bias_type, const void *bias_dev,
+                        int32_t residual_type, const void *residual_dev, int64_t residual_stride,
+                        int32_t out_type, void *out_dev, int64_t out_stride, void *stream);
+
+/* Bytes of device workspace moe_routed_prefill needs (0 for sizes it
+ * refuses). */
+int64_t moe_routed_prefill_workspace_bytes(int32_t weight_format, int32_t num_rows, int32_t hidden,
+                                           int32_t ffn, int32_t T, int32_t K);
+
+/* moe_routed_decode for prompts: the routes sorted by row, one grouped product
+ * for gate and up with SwiGLU (rounded to bf16), one for down (fp32), and the
+ * combine
+ *   out[t] = bf16( sum over k ascending with a valid row of w[t][k] y[t][k]
+ *                  + addend[t] ).
+ * Any of the three formats, any widths (4 bits: multiples of 32), up to
+ * 2^22 routes; sums are taken in another order than moe_routed_decode's.
+ * Arguments as moe_routed_decode.  Errors: as moe_grouped_product;
+ * MOE_UNSUPPORTED (hidden or ffn > 2^16, T > 65535, K > 64). */
+moe_status_t moe_routed_prefill(const moe_pool_t *pool, const void *x_dev, const int32_t *idx_dev,
+                                const float *w_dev, int32_t T, int32_t K, const float *addend_dev,
+                                void *out_dev, void *workspace_dev, int64_t workspace_bytes,
+                                void *stream);
+
 /* ---------------------------------------------------------------- inspection */
 
 /* Copies the layer's statistics (layer = -1: sums over layers) into
