@@ -461,7 +461,7 @@ def _on_current_device(*tensors):
     """The library launches on the current device: every tensor must be on it.  Returns its index."""
     if _torch is None:
         _load_torch()
-    dev = _torch.cuda.current_device()
+    dev = _torch._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"expected tensors on the current device cuda:{dev}, got {t.device}")
@@ -688,37 +688,53 @@ def moe_group_routes(idx, num_rows: int, offsets, order, workspace=None, stream=
     _want(idx, "idx", (T, K), _I32)
     _want(offsets, "offsets", (num_rows + 1,), _I32)
     _want(order, "order", (T * K,), _I32)
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _check(lib().moe_group_routes(
-        idx.data_ptr(), T, K, num_rows, offsets.data_ptr(), order.data_ptr(),
-        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
-        _stream_on(dev, stream)))
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    _check(lib().moe_group_routes(idx.data_ptr(), T, K, num_rows, offsets.data_ptr(), order.data_ptr(), ws, ws_bytes,
+                                  _stream_on(dev, stream)))
 
 
-def _product_rows(bank, x, out, activation, bias, bias_shape, dev):
-    """(rows of x, their stride, rows of out, their stride, bias type, out type)."""
-    x_rows, k, x_stride = _rows_of(x, "x")
+def _product_rows(bank, x, out, activation):
+    """(device, rows of x, their stride, rows of out, their stride, out type), everything checked."""
+    dev = _on_current_device(x, out)
+    if bank._device != dev:
+        _on_current_device(*bank._keep)
+    x_shape, out_shape = x.shape, out.shape
+    if len(x_shape) != 2 or len(out_shape) != 2:
+        raise ValueError("x and out: expected 2-d tensors")
+    x_rows, k = x_shape
+    out_rows, cols = out_shape
+    x_stride, x_step = x.stride()
+    out_stride, out_step = out.stride()
+    if (x_step != 1 and k > 1) or (out_step != 1 and cols > 1):
+        raise ValueError("x and out: expected contiguous rows")
     if k != bank.k:
         raise ValueError(f"x has {k} columns, the bank's matrices {bank.k}")
-    if _type_of(x, "x") != MOE_TYPE_BF16:
-        raise ValueError("x must be bfloat16")
-    out_rows, cols, out_stride = _rows_of(out, "out")
     if cols != (bank.n // 2 if activation == MOE_ACT_SWIGLU else bank.n):
         raise ValueError(f"out has {cols} columns for matrices of {bank.n} rows")
-    if getattr(bank, "_device", None) != dev:
-        _on_current_device(*getattr(bank, "_keep", ()))
-        bank._device = dev
-    bias_type = 0
-    if bias is not None:
-        _want(bias, "bias", bias_shape)
-        bias_type = _type_of(bias, "bias")
-    return x_rows, x_stride, out_rows, out_stride, bias_type, _type_of(out, "out")
+    if _TYPES.get(x.dtype) != MOE_TYPE_BF16:
+        raise ValueError("x must be bfloat16")
+    out_type = _TYPES.get(out.dtype)
+    if out_type is None:
+        _type_of(out, "out")
+    # a single row has no stride of its own
+    return dev, x_rows, x_stride if x_rows > 1 else k, out_rows, out_stride if out_rows > 1 else cols, out_type
 
 
-def _indices(t, what, n):
-    if t is None:
-        return None
+def _bias_of(bias, shape, dev):
+    """(pointer, type)."""
+    if bias.get_device() != dev:
+        _on_current_device(bias)
+    _want(bias, "bias", shape)
+    return bias.data_ptr(), _type_of(bias, "bias")
+
+
+def _indices(t, what, n, dev):
+    if t.get_device() != dev:
+        _on_current_device(t)
     _want(t, what, (n,), _I32)
     return t.data_ptr()
 
@@ -729,16 +745,26 @@ def moe_grouped_product(bank: moe_bank_t, x, offsets, out, matrices=None, gather
     be strided), offsets int32 [G + 1], matrices int32 [G]; gather and scatter
     int32 [R], where R is their length, or the rows of x without gather and
     scatter; bias [num_rows, n]."""
-    dev = _on_current_device(x, offsets, out, matrices, gather, scatter, bias)
-    x_rows, x_stride, out_rows, out_stride, bias_type, out_type = _product_rows(
-        bank, x, out, activation, bias, (bank.num_rows, bank.n), dev)
-    R = x_rows if gather is None and scatter is None else (gather if gather is not None else scatter).numel()
+    dev, x_rows, x_stride, out_rows, out_stride, out_type = _product_rows(bank, x, out, activation)
+    R = x_rows
+    if gather is not None:
+        R = gather.numel()
+        gather = _indices(gather, "gather", R, dev)
+        if scatter is not None:
+            scatter = _indices(scatter, "scatter", R, dev)
+    elif scatter is not None:
+        R = scatter.numel()
+        scatter = _indices(scatter, "scatter", R, dev)
     G = offsets.numel() - 1
+    offsets = _indices(offsets, "offsets", G + 1, dev)
+    if matrices is not None:
+        matrices = _indices(matrices, "matrices", G, dev)
+    bias_type = 0
+    if bias is not None:
+        bias, bias_type = _bias_of(bias, (bank.num_rows, bank.n), dev)
     _check(lib().moe_grouped_product(
-        C.byref(bank), x.data_ptr(), x_stride, x_rows, _indices(offsets, "offsets", G + 1), G,
-        _indices(matrices, "matrices", G), _indices(gather, "gather", R), gather_div,
-        _indices(scatter, "scatter", R), R, activation, bias_type, None if bias is None else bias.data_ptr(),
-        out_type, out.data_ptr(), out_stride, out_rows, _stream_on(dev, stream)))
+        C.byref(bank), x.data_ptr(), x_stride, x_rows, offsets, G, matrices, gather, gather_div, scatter, R,
+        activation, bias_type, bias, out_type, out.data_ptr(), out_stride, out_rows, _stream_on(dev, stream)))
 
 
 def moe_linear(bank: moe_bank_t, x, out, activation: int = MOE_ACT_NONE, bias=None, residual=None,
@@ -746,21 +772,23 @@ def moe_linear(bank: moe_bank_t, x, out, activation: int = MOE_ACT_NONE, bias=No
     """out = act(x W^T + bias) + residual: x [T, k] bfloat16, out [T, n or
     n/2] float32 or bfloat16, bias [n], residual shaped as out (it may be out);
     rows of x, out and residual may be strided."""
-    dev = _on_current_device(x, out, bias, residual)
-    T, x_stride, out_rows, out_stride, bias_type, out_type = _product_rows(
-        bank, x, out, activation, bias, (bank.n,), dev)
+    dev, T, x_stride, out_rows, out_stride, out_type = _product_rows(bank, x, out, activation)
     if out_rows != T:
         raise ValueError(f"out has {out_rows} rows for {T} of x")
+    bias_type = 0
+    if bias is not None:
+        bias, bias_type = _bias_of(bias, (bank.n,), dev)
     res, res_type, res_stride = None, 0, 0
     if residual is not None:
         if residual.shape != out.shape:
             raise ValueError(f"residual: expected the shape of out {tuple(out.shape)}, got {tuple(residual.shape)}")
+        if residual.get_device() != dev:
+            _on_current_device(residual)
         res, res_type, res_stride = residual.data_ptr(), _type_of(residual, "residual"), \
             _rows_of(residual, "residual")[2]
     _check(lib().moe_linear(
-        C.byref(bank), x.data_ptr(), x_stride, T, activation, bias_type,
-        None if bias is None else bias.data_ptr(), res_type, res, res_stride, out_type, out.data_ptr(),
-        out_stride, _stream_on(dev, stream)))
+        C.byref(bank), x.data_ptr(), x_stride, T, activation, bias_type, bias, res_type, res, res_stride, out_type,
+        out.data_ptr(), out_stride, _stream_on(dev, stream)))
 
 
 def moe_routed_prefill_workspace_bytes(weight_format: int, num_rows: int, hidden: int, ffn: int, T: int,

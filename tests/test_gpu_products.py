@@ -560,3 +560,15 @@ def test_layers_prefill_through_the_streamed_experts():
             assert np.abs(_f64(out) - _f64(e)).max() <= 2.0 ** -6 * np.abs(_f64(e)).max()
     finally:
         lay.close()
+
+
+@pytest.mark.parametrize("T,K,P", [(1 << 16, 64, 300), (1 << 19, 8, 4095), (1 << 18, 4, 4096)])
+def test_lists_of_many_routes(T, K, P):
+    """Up to the most routes, on both sides of the rows that waves count alone."""
+    _say("many lists", T, K, P)
+    g = W.rng(99, "many", T, P)
+    idx = (g.random((T, K)) ** 3 * (P + 1)).astype(np.int32) - 1
+    offsets, order = _lists(_i32(idx), P)
+    key = np.where(idx.reshape(-1) < 0, P, idx.reshape(-1))
+    assert (offsets.cpu().numpy() == np.searchsorted(np.sort(key), np.arange(P + 1))).all()
+    assert (order.cpu().numpy() == np.argsort(key, kind="stable")).all()
