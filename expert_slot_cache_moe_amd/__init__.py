@@ -143,6 +143,8 @@ def lib():
                                          i32, P]),
             "moe_linear": (st, [P, P, i64, i32, i32, i32, P, i32, P, i64, i32, P, i64, P]),
             "moe_routed_prefill_workspace_bytes": (i64, [i32, i32, i32, i32, i32, i32]),
+            "moe_shared_prefill_workspace_bytes": (i64, [i32, i32, i32]),
+            "moe_shared_prefill": (st, [P, i32, P, i32, P, P, i64, P]),
             "moe_routed_prefill": (st, [P, P, P, P, i32, i32, P, P, P, i64, P]),
         }
         for name, (res, args) in sig.items():
@@ -811,6 +813,22 @@ def moe_routed_prefill(pool: moe_pool_t, x, idx, w, out, workspace, addend=None,
     _check(lib().moe_routed_prefill(
         C.byref(pool), _dev_ptr(x), _dev_ptr(idx), _dev_ptr(w), T, K, _dev_ptr(addend), _dev_ptr(out),
         _dev_ptr(workspace), workspace.nbytes, _stream_on(dev, stream)))
+
+
+def moe_shared_prefill_workspace_bytes(hidden: int, ffn: int, T: int) -> int:
+    return int(lib().moe_shared_prefill_workspace_bytes(hidden, ffn, T))
+
+
+def moe_shared_prefill(shared: moe_shared_t, hidden: int, x, addend, workspace, stream=None) -> None:
+    """moe_shared_expert for prompts."""
+    T = x.shape[0]
+    dev = _on_current_device(x, addend, workspace)
+    if _type_of(x, "x") != MOE_TYPE_BF16:
+        raise ValueError("x must be bfloat16")
+    _want(x, "x", (T, hidden))
+    _want(addend, "addend", (T, hidden), _F32)
+    _check(lib().moe_shared_prefill(C.byref(shared), hidden, _dev_ptr(x), T, _dev_ptr(addend), _dev_ptr(workspace),
+                                    workspace.nbytes, _stream_on(dev, stream)))
 
 
 # ---------------------------------------------------------------- inspection

@@ -1,6 +1,6 @@
 // Host-side internals shared by the C ABI's sources (moe_api.hip,
-// moe_layer.hip, moe_prefetch.hip, moe_operators.hip): error reporting, the cache object, and
-// the launch sequences several entry points share.  Not part of the ABI.
+// moe_layer.hip, moe_prefetch.hip, moe_operators.hip, moe_products.hip): error
+// reporting, the cache object, and the launch sequences several entry points share.  Not part of the ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>

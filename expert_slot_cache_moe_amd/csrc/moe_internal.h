@@ -406,6 +406,7 @@ struct ProductParams {
     int32_t act;
     const void *bias;                // [P][n] or NULL
     int32_t bias_type;
+    const float *gate;               // [out_rows] or NULL: row r's sums are taken times sigmoid(gate[r])
     const void *residual;            // [out_rows][cols] or NULL
     int32_t res_type;
     int64_t res_stride;

@@ -1,6 +1,6 @@
 // The C ABI (include/moe_cache.h), part 5: lists of routes by matrix row,
-// products grouped by matrix, dense products, and the routed experts of a
-// prompt made of them.  Checks on the host, then launches; nothing here
+// products grouped by matrix, dense products, and the routed and shared experts
+// of a prompt made of them.  Checks on the host, then launches; nothing here
 // synchronises or allocates.
 #include <algorithm>
 
@@ -116,6 +116,25 @@ PrefillWs prefill_ws(int P, int H, int F, int T, int K) {
     w.d = w.h + align_up(n * F * 2);
     w.total = w.d + align_up(n * H * 4);
     return w;
+}
+
+// The activations of every token, and what its gate says.
+struct SharedWs {
+    size_t h, gate, total;
+};
+SharedWs shared_ws(int F, int T) {
+    SharedWs w;
+    w.h = 0;
+    w.gate = align_up((size_t)T * F * 2);
+    w.total = w.gate + align_up((size_t)T * 4);
+    return w;
+}
+
+moe_status_t check_shared_prefill(int32_t H, int32_t F, int32_t T) {
+    if (H < 1 || F < 1 || T < 0) return fail(MOE_INVALID_ARG, "shared expert: hidden %d / ffn %d, T=%d", H, F, T);
+    if (H > kProductMaxK || F > kProductMaxK || T > kProductMaxPlaces)
+        return fail(MOE_UNSUPPORTED, "shared expert: hidden %d / ffn %d, T=%d", H, F, T);
+    return MOE_OK;
 }
 
 }  // namespace
@@ -244,6 +263,53 @@ moe_status_t moe_routed_prefill(const moe_pool_t *pool, const void *x, const int
     HIP_TRY(launch_product(up, s), "gate/up product launch");
     HIP_TRY(launch_product(down, s), "down product launch");
     HIP_TRY(launch_combine(idx, w, T, K, H, P, d, addend, static_cast<uint16_t *>(out), s), "combine launch");
+    return MOE_OK;
+}
+
+int64_t moe_shared_prefill_workspace_bytes(int32_t H, int32_t F, int32_t T) {
+    if (check_shared_prefill(H, F, T) != MOE_OK) return 0;
+    return (int64_t)shared_ws(F, T).total;
+}
+
+moe_status_t moe_shared_prefill(const moe_shared_t *sh, int32_t H, const void *x, int32_t T, float *addend, void *ws,
+                                int64_t ws_bytes, void *stream) {
+    if (!sh) return fail(MOE_INVALID_ARG, "shared expert is NULL");
+    const int F = sh->ffn;
+    moe_status_t st = check_shared_prefill(H, F, T);
+    if (st != MOE_OK) return st;
+    if (!sh->w13_dev || !sh->w2_dev || !sh->gate_dev)
+        return fail(MOE_INVALID_ARG, "shared expert has a NULL weight");
+    if (T > 0 && (!x || !addend || !ws)) return fail(MOE_INVALID_ARG, "NULL shared buffer");
+    if (misaligned(ws, 256)) return fail(MOE_INVALID_ARG, "workspace must be 256-byte aligned");
+    const SharedWs L = shared_ws(F, T);
+    if (ws_bytes < (int64_t)L.total)
+        return fail(MOE_INVALID_ARG, "workspace %lld B < %zu B", (long long)ws_bytes, L.total);
+    uint16_t *h = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + L.h);
+    float *logits = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + L.gate);
+    auto bank = [](const void *w, int n, int k) {
+        moe_bank_t b{};
+        b.weight_format = MOE_FMT_BF16;
+        b.num_rows = 1;
+        b.n = n;
+        b.k = k;
+        b.weights_dev = w;
+        return b;
+    };
+    const moe_bank_t gate_bank = bank(sh->gate_dev, 1, H), up_bank = bank(sh->w13_dev, 2 * F, H),
+                     down_bank = bank(sh->w2_dev, H, F);
+    ProductParams gate, up, down;
+    st = check_product(&gate_bank, T, MOE_ACT_NONE, 0, nullptr, MOE_TYPE_F32, logits, 1, x, H, gate);
+    if (st == MOE_OK) st = check_product(&up_bank, T, MOE_ACT_SWIGLU, 0, nullptr, MOE_TYPE_BF16, h, F, x, H, up);
+    if (st == MOE_OK) st = check_product(&down_bank, T, MOE_ACT_NONE, 0, nullptr, MOE_TYPE_F32, addend, H, h, F, down);
+    if (st != MOE_OK || T == 0) return st;
+    down.gate = logits;
+    for (const ProductParams *p : {&gate, &up, &down})
+        if (!product_launchable(*p))
+            return fail(MOE_UNSUPPORTED, "%d tokens of hidden %d, ffn %d: too many tiles", T, H, F);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    HIP_TRY(launch_product(gate, s), "shared gate launch");
+    HIP_TRY(launch_product(up, s), "shared gate/up product launch");
+    HIP_TRY(launch_product(down, s), "shared down product launch");
     return MOE_OK;
 }
 

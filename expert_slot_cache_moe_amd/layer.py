@@ -10,8 +10,8 @@ import torch
 from . import (MOE_FMT_BF16, MOE_FMT_E2M1, make_pool, make_shared, moe_bank_row_bytes,
                moe_cache_create, moe_cache_destroy, moe_layer_decode, moe_layer_decode_hybrid,
                moe_layer_decode_router, moe_quantize_rows, moe_route, moe_routed_prefill,
-               moe_routed_prefill_workspace_bytes, moe_routed_workspace_bytes, moe_shared_expert,
-               moe_topk)
+               moe_routed_prefill_workspace_bytes, moe_shared_prefill,
+               moe_shared_prefill_workspace_bytes, moe_topk)
 
 
 def pinned(a: np.ndarray) -> torch.Tensor:
@@ -125,9 +125,19 @@ class SlotCacheLayers:
         """A prompt's rows through all of the layer's experts, on the current
         stream: the routes of decode(), the shared expert, and
         moe_routed_prefill over `pool` (streamed_pool(layer), copied here if
-        not given).  The cache and its statistics stay as they are; any number
-        of tokens up to 65535."""
+        not given, which a capture cannot hold).  The cache and its statistics
+        stay as they are; any number of tokens up to 65535."""
+        if not 0 <= layer < self.L:
+            raise ValueError(f"layer {layer} outside [0, {self.L})")
         T = x.shape[0]
+        for name, t, shape in (("x", x, (T, self.H)), ("logits", logits, (T, self.E)), ("out", out, (T, self.H)),
+                               ("ids_out", ids_out, (T, K)), ("w_out", w_out, (T, K))):
+            if t is not None and tuple(t.shape) != shape:
+                raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+        for name, t, dtype in (("logits", logits, torch.float32), ("ids_out", ids_out, torch.int32),
+                               ("w_out", w_out, torch.float32)):
+            if t is not None and t.dtype != dtype:
+                raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
         ids = torch.empty((T, K), dtype=torch.int32, device=self.device) if ids_out is None else ids_out
         w = torch.empty((T, K), dtype=torch.float32, device=self.device) if w_out is None else w_out
         if self.routers[layer] is None:
@@ -137,8 +147,8 @@ class SlotCacheLayers:
         shared, addend = self._shared(layer), None
         if shared is not None:
             addend = torch.empty((T, self.H), dtype=torch.float32, device=self.device)
-            n = moe_routed_workspace_bytes(MOE_FMT_BF16, self.H, shared.ffn, T, 1)
-            moe_shared_expert(shared, self.H, x, addend, torch.empty(n, dtype=torch.uint8, device=self.device))
+            n = moe_shared_prefill_workspace_bytes(self.H, shared.ffn, T)
+            moe_shared_prefill(shared, self.H, x, addend, torch.empty(n, dtype=torch.uint8, device=self.device))
         if pool is None:
             pool = self.streamed_pool(layer)
         n = moe_routed_prefill_workspace_bytes(self.fmt, pool.num_rows, self.H, self.F, T, K)

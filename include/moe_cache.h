@@ -608,8 +608,9 @@ moe_status_t moe_group_routes(const int32_t *idx_dev, int32_t T, int32_t K, int3
  * gate/up product gathers (gather = order, gather_div = K) and a down product
  * scatters (scatter = order).
  *  - Sums, bias and activation are fp32, rounded once to out_type; 4-bit
- *    weights are multiplied at their exact values (an E2M1 matrix's global
- *    scale multiplies the sum), a NaN scale makes the outputs it reaches NaN.
+ *    weights are multiplied at their exact values (from 2^128 on infinity; an
+ *    E2M1 matrix's global scale multiplies the sum), a NaN scale makes the
+ *    outputs it reaches NaN.
  *  - A group whose matrix is outside [0, num_rows) gets rows of zeros.
  *  - Places in no group, places whose row of x is outside [0, x_rows) and
  *    places whose row of out is outside [0, out_rows) are left out: nothing is
@@ -663,6 +664,23 @@ int64_t moe_routed_prefill_workspace_bytes(int32_t weight_format, int32_t num_ro
 moe_status_t moe_routed_prefill(const moe_pool_t *pool, const void *x_dev, const int32_t *idx_dev,
                                 const float *w_dev, int32_t T, int32_t K, const float *addend_dev,
                                 void *out_dev, void *workspace_dev, int64_t workspace_bytes,
+                                void *stream);
+
+/* Bytes of device workspace moe_shared_prefill needs (0 for sizes it
+ * refuses). */
+int64_t moe_shared_prefill_workspace_bytes(int32_t hidden, int32_t ffn, int32_t T);
+
+/* moe_shared_expert for prompts, in three dense products: the gate's logits
+ * (fp32), gate and up with SwiGLU (rounded to bf16), and down, whose sums are
+ * taken times sigmoid(logit) in fp32:
+ *   addend[t] = sigmoid(x_t . gate) * shared(x_t), fp32 [T][H],
+ * the addend of moe_routed_prefill.  Any widths; sums are taken in another
+ * order than moe_shared_expert's.  shared->ffn must be set.  Errors:
+ * MOE_INVALID_ARG (sizes, null or misaligned pointers: 2 bytes for weights and
+ * x, 4 for addend, 256 for the workspace), MOE_UNSUPPORTED (hidden or ffn >
+ * 2^16, T > 2^22, or so many tiles that a launch would have 2^32 threads). */
+moe_status_t moe_shared_prefill(const moe_shared_t *shared, int32_t hidden, const void *x_dev, int32_t T,
+                                float *addend_dev, void *workspace_dev, int64_t workspace_bytes,
                                 void *stream);
 
 /* ---------------------------------------------------------------- inspection */
