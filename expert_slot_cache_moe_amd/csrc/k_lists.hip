@@ -17,7 +17,8 @@
 // Up to kOneBlock routes one block does all; above, a launch counts each
 // piece's routes and a second places them, each block summing the counts of
 // the pieces before it.  Bound by latency: 2 x 4 bytes a route are read and
-// 4 written (163840 routes: 2 MB).
+// 4 written (163840 routes over 512 rows, 2 MB: 2.4 + 11.6 us; one token's 8
+// over 256 3.1).
 #include <algorithm>
 
 #include "moe_internal.h"

@@ -17,27 +17,27 @@ int64_t even_blocks(const ProductParams &p, int form) {
 
 // Up to so many blocks of the split form: it has one launch's latency, where
 // a tile passes all of k stage by stage (dense bf16, us, split / 32 places:
-// 256 blocks of k 2048 6.3 / 12.1, 512 10.3 / 12.1, 1024 18.5 / 12.2; 512 of k
-// 4096 17.6 / 29.9, 1024 33.1 / 30.1; 512 of k 1024 6.8 / 8.2, 1024 11.5 /
-// 8.3).  With rows of x that are no whole vectors of eight fewer (k 1061, 132
-// blocks 9.3 / 12.4, 264 14.3 / 12.5), with 4-bit weights more (MXFP4, k 1056,
-// 792 blocks 8.6 / 10.5; k 1024, 1024 blocks 9.5 / 8.3).
+// 256 blocks of k 2048 6.2 / 12.0, 512 10.3 / 14.4, 1024 18.7 / 14.6; 512 of k
+// 4096 17.8 / 25.3, 1024 33.2 / 26.2; 1024 of k 1024 11.6 / 10.3, 2048 21.1 /
+// 12.2).  With rows of x that are no whole vectors of eight fewer (k 1061, 128
+// blocks 9.2 / 9.5, 512 16.5 / 9.7), with 4-bit weights more (MXFP4, k 1056,
+// 528 blocks 8.2 / 10.0; k 1024, 1024 blocks 9.2 / 8.7).
 constexpr int64_t kSplitBlocks = 512, kSplitBlocksCut = 192, kSplitBlocksCodes = 800;
 // The mean places of a matrix from which a tile of 64, 128, 256 places pays
-// (bf16, 64 matrices of 2048 x 2048, us at 32 / 64 / 128 / 256 places: mean 4
-// 122 117 122 137, 32 128 122 129 144, 64 191 127 142 151, 96 254 153 141
-// 186, 192 439 254 177 192, 256 574 324 226 205; 160 of 512 x 1024: mean 8 27
-// 28 32 59, 16 29 29 33 60, 64 63 42 40 68, 96 81 55 44 70, 256 163 110 84
-// 82), and for 4 bits one of 64 (E2M1, 64 of 2048 x 2048, 32 / 64 places: mean
-// 32 53 60, 48 68 64, 96 127 101).
+// (bf16, 64 matrices of 2048 x 2048, us at 32 / 64 / 128 / 256 places: mean 8
+// 126 121 128 148, 32 128 121 129 149, 64 191 126 141 152, 96 258 153 141 195,
+// 192 438 253 179 193, 256 572 326 222 203; 160 of 512 x 1024: mean 8 28 29 33
+// 66, 16 29 30 35 66, 64 64 41 40 67, 96 81 54 43 68, 256 163 110 82 74), and
+// for 4 bits one of 64 (E2M1, 64 of 2048 x 2048, 32 / 64 places: mean 32 52
+// 60, 48 67 63, 96 117 98).
 constexpr int64_t kMean64 = 12, kMean128 = 72, kMean256 = 224, kMeanCodes64 = 40;
 // A larger tile is taken only where there is a block for each of the 256 CUs
-// (dense 4096 x 4096, us at 64 / 128 / 256 places: 512 rows 42 45 106, 1024 62
-// 48 106, 2048 140 79 107, 4096 284 157 136), or for half of them where each
+// (dense 4096 x 4096, us at 64 / 128 / 256 places: 512 rows 41 41 92, 1024 56
+// 44 98, 2048 139 76 97, 4096 281 151 120), or for half of them where each
 // piece more reads a matrix of its own again (32 / 64 places, 128 and 132
-// blocks of 64: 8 matrices of 1024 x 2048 27.7 / 19.3, 33 of 138 x 2656 33.6 /
-// 25.9, 66 blocks 22.5 / 24.4; a dense 1024 x 1024 of 128 blocks 8.7 / 11.3;
-// MXFP4, 24 of 515 x 1056, 240 blocks 19.0 / 22.0).
+// blocks of 64: 8 matrices of 1024 x 2048 22.4 / 17.6, 33 of 138 x 2656 22.1 /
+// 23.3; a dense 1024 x 1024 of 128 blocks 8.1 / 9.3; MXFP4, 24 of 515 x 1056,
+// 240 blocks 13.3 / 13.4).
 constexpr int64_t kEnoughBlocks = 256, kEnoughBlocksGrouped = 120;
 
 int form_of(const ProductParams &p) {
