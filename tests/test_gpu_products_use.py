@@ -253,3 +253,49 @@ def test_activations_at_their_ends(act, T):
     fin = np.isfinite(y)
     assert (np.abs(got[0] - val[0])[fin] <= bnd[0][fin] + np.abs(val[0][fin]) * 2.0 ** -23 + 2.0 ** -126).all()
     assert np.isnan(got[0][np.isnan(y)]).all() and (got[0][y == np.inf] == np.inf).all()
+
+
+# ---------------------------------------------------------------- short rows of 4 bits
+
+def _decoded(g, fmt, P, n, k):
+    """A bank of random codes and finite scales, its parts, and its values."""
+    values = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+    codes = g.integers(0, 256, (P, n, k // 2)).astype(np.uint8)
+    if fmt == m.MOE_FMT_E2M1:
+        sc = g.integers(0x28, 0x48, (P, n, k // 16)).astype(np.uint8)
+        scale = np.repeat((8 + (sc & 7)) * 2.0 ** ((sc >> 3).astype(float) - 10), 16, -1)
+    else:
+        sc = g.integers(122, 130, (P, n, k // 32)).astype(np.uint8)
+        scale = np.repeat(2.0 ** (sc.astype(float) - 127), 32, -1)
+    nib = np.stack([codes & 15, codes >> 4], -1).reshape(P, n, k)
+    return codes, sc, np.where(nib & 8, -1.0, 1.0) * values[nib & 7] * scale
+
+
+@pytest.mark.parametrize("fmt", [m.MOE_FMT_E2M1, m.MOE_FMT_MXFP4])
+@pytest.mark.parametrize("P,n,k,R", [(1, 4, 32, 17000), (1, 130, 32, 3000), (120, 96, 32, 2400), (2, 67, 64, 5000),
+                                     (120, 96, 64, 2400), (3, 257, 96, 3100), (130, 60, 96, 4000), (1, 16, 128, 16000)])
+def test_rows_shorter_than_a_span(fmt, P, n, k, R):
+    g = W.rng(118, fmt, P, n, k, R)
+    codes, sc, w = _decoded(g, fmt, P, n, k)
+    bank = m.make_bank(fmt, torch.from_numpy(codes).cuda(), torch.from_numpy(sc).cuda())
+    x = _bf16(g, (R, k))
+    offsets = np.concatenate([[0], np.sort(g.integers(0, R + 1, P - 1)), [R]]).astype(np.int32)
+    out = torch.full((R, n), 77.0, device="cuda")
+    m.moe_grouped_product(bank, x, _i32(offsets), out)
+    done, val, bnd = ref.grouped(w, _f64(x), offsets, R)
+    assert done.all() and ref.off(_f64(out), val, bnd, "float32") <= 0
+
+
+@pytest.mark.parametrize("fmt,bad", [(m.MOE_FMT_E2M1, 0x7f), (m.MOE_FMT_MXFP4, 0xff)])
+@pytest.mark.parametrize("k", [32, 64, 96])
+def test_nan_scales_of_short_rows_stay_in_them(fmt, bad, k):
+    P, n, R = 2, 70, 4000
+    g = W.rng(119, fmt, k)
+    codes, sc, _ = _decoded(g, fmt, P, n, k)
+    sc[0, 1] = sc[0, 69] = sc[1, 0] = sc[1, 5] = bad
+    bank = m.make_bank(fmt, torch.from_numpy(codes).cuda(), torch.from_numpy(sc).cuda())
+    out = torch.zeros((R, n), device="cuda")
+    m.moe_grouped_product(bank, _bf16(g, (R, k)), _i32([0, 2100, R]), out)
+    nan = np.zeros((R, n), bool)
+    nan[:2100, [1, 69]] = nan[2100:, [0, 5]] = True
+    assert np.array_equal(np.isnan(_f64(out)), nan)
