@@ -42,7 +42,7 @@ constexpr int64_t kEnoughBlocks = 256, kEnoughBlocksGrouped = 120;
 
 int form_of(const ProductParams &p) {
     const bool wide = p.fmt == MOE_FMT_BF16;
-    if (p.k < kTileMinK || p.n / (p.act == MOE_ACT_SWIGLU ? 2 : 1) < kTileMinCols) return kSplit;
+    if (p.n / (p.act == MOE_ACT_SWIGLU ? 2 : 1) < kTileMinCols) return kSplit;
     const bool cut = p.k % 8 != 0 || p.x_stride % 8 != 0;
     if (even_blocks(p, kSplit) <= (!wide ? kSplitBlocksCodes : cut ? kSplitBlocksCut : kSplitBlocks)) return kSplit;
     const int64_t groups = p.offsets == nullptr ? 1 : std::min(p.G, p.R), mean = p.R / groups;

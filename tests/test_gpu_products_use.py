@@ -299,3 +299,22 @@ def test_nan_scales_of_short_rows_stay_in_them(fmt, bad, k):
     nan = np.zeros((R, n), bool)
     nan[:2100, [1, 69]] = nan[2100:, [0, 5]] = True
     assert np.array_equal(np.isnan(_f64(out)), nan)
+
+
+# ---------------------------------------------------------------- rows shorter than a vector
+
+@pytest.mark.parametrize("k", [1, 3, 7])
+@pytest.mark.parametrize("P,n,R,act", [(300, 40, 600, "none"), (40, 600, 1600, "swiglu"), (60, 300, 6000, "none"),
+                                       (1, 2100, 8192, "none"), (1, 2100, 8192, "swiglu"), (1, 3, 9000, "none")])
+def test_bf16_rows_shorter_than_a_vector(P, n, k, R, act):
+    """A tile reads eight elements at once: here there are fewer, and the buffers end with the last row."""
+    print("short rows", P, n, k, R, act, flush=True)
+    g = W.rng(120, P, n, k, R, act)
+    w, x = _bf16(g, (P, n, k)), _bf16(g, (R, k))
+    cols = n // 2 if act == "swiglu" else n
+    offsets = np.concatenate([[0], np.sort(g.integers(0, R + 1, P - 1)), [R]]).astype(np.int32)
+    out = torch.full((R, cols), 77.0, device="cuda")
+    m.moe_grouped_product(m.make_bank(m.MOE_FMT_BF16, w), x, _i32(offsets), out,
+                          activation=m.MOE_ACT_SWIGLU if act == "swiglu" else m.MOE_ACT_NONE)
+    done, val, bnd = ref.grouped(_f64(w), _f64(x), offsets, R, act=act)
+    assert done.all() and ref.off(_f64(out), val, bnd, "float32") <= 0
