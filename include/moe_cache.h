@@ -617,8 +617,9 @@ moe_status_t moe_group_routes(const int32_t *idx_dev, int32_t T, int32_t K, int3
  *    written for them.  Rows of out that no place names stay as they were.
  *  - offsets ascend from at least 0 to at most R (others are cut to that
  *    range); two places must not name one row of out.
- * Within a call a place's result depends on its matrix's bytes and its x
- * alone; calls of other sizes may add in another order.
+ * Within a call a place's result depends on its matrix (its bytes, and its
+ * number in the bank) and its x alone; calls of other sizes may add in another
+ * order.
  * x_dev: bf16 [x_rows] rows, x_stride elements apart; bias_dev: [num_rows][n]
  * of bias_type, or NULL; out_dev: [out_rows] rows of n (SWIGLU: n/2) of
  * out_type, out_stride elements apart, the gaps not written; offsets_dev:
