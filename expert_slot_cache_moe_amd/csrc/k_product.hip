@@ -25,11 +25,11 @@ int64_t even_blocks(const ProductParams &p, int form) {
 constexpr int64_t kSplitBlocks = 512, kSplitBlocksCut = 192, kSplitBlocksCodes = 800;
 // The mean places of a matrix from which a tile of 64, 128, 256 places pays
 // (bf16, 64 matrices of 2048 x 2048, us at 32 / 64 / 128 / 256 places: mean 8
-// 126 121 128 148, 32 128 121 129 149, 64 191 126 141 152, 96 258 153 141 195,
-// 192 438 253 179 193, 256 572 326 222 203; 160 of 512 x 1024: mean 8 28 29 33
-// 66, 16 29 30 35 66, 64 64 41 40 67, 96 81 54 43 68, 256 163 110 82 74), and
-// for 4 bits one of 64 (E2M1, 64 of 2048 x 2048, 32 / 64 places: mean 32 52
-// 60, 48 67 63, 96 117 98).
+// 96 96 95 132, 16 103 97 96 128, 48 156 107 115 134, 64 195 117 116 136, 96
+// 261 153 126 187, 192 444 253 176 197, 256 578 326 224 201; 160 of 512 x
+// 1024: mean 8 27 28 34 64, 16 29 30 34 64, 64 64 40 41 66, 96 80 55 44 67,
+// 256 161 110 82 79), and for 4 bits one of 64 (E2M1, 64 of 2048 x 2048, 32 /
+// 64 places: mean 32 52 60, 48 67 63, 96 117 98).
 constexpr int64_t kMean64 = 12, kMean128 = 72, kMean256 = 224, kMeanCodes64 = 40;
 // A larger tile is taken only where there is a block for each of the 256 CUs
 // (dense 4096 x 4096, us at 64 / 128 / 256 places: 512 rows 41 41 92, 1024 56
