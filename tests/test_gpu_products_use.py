@@ -318,3 +318,18 @@ def test_bf16_rows_shorter_than_a_vector(P, n, k, R, act):
                           activation=m.MOE_ACT_SWIGLU if act == "swiglu" else m.MOE_ACT_NONE)
     done, val, bnd = ref.grouped(_f64(w), _f64(x), offsets, R, act=act)
     assert done.all() and ref.off(_f64(out), val, bnd, "float32") <= 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,n,k", [(3, 5, 40), (700, 515, 72), (900, 130, 264), (5000, 1027, 64), (9000, 3, 64)])
+def test_odd_rows_of_residuals_in_place(T, n, k, dtype):
+    """out as its own residual, rows of an odd number of columns: as with a copy of it, and nothing beside the rows."""
+    g = W.rng(121, T, n, k, dtype)
+    bank = m.make_bank(m.MOE_FMT_BF16, _bf16(g, (1, n, k)))
+    x, res = _bf16(g, (T, k)), _bf16(g, (T, n + 2)).to(dtype)
+    out, place = torch.zeros((T, n), dtype=dtype, device="cuda"), res.clone()
+    m.moe_linear(bank, x, out, residual=res[:, :n], activation=m.MOE_ACT_SILU)
+    m.moe_linear(bank, x, place[:, :n], residual=place[:, :n], activation=m.MOE_ACT_SILU)
+    assert torch.equal(place[:, :n], out) and torch.equal(place[:, n:], res[:, n:])
+    val, bnd = ref.product(_f64(bank._keep[0])[0], _f64(x), "silu", residual=_f64(res[:, :n]))
+    assert ref.off(_f64(out), val, bnd, str(dtype).split(".")[1]) <= 0
