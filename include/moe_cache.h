@@ -607,10 +607,12 @@ moe_status_t moe_group_routes(const int32_t *idx_dev, int32_t T, int32_t K, int3
  * scatter[i], or i without scatter.  With the lists of moe_group_routes a
  * gate/up product gathers (gather = order, gather_div = K) and a down product
  * scatters (scatter = order).
- *  - Sums, bias and activation are fp32, rounded once to out_type; 4-bit
- *    weights are multiplied at their exact values (from 2^128 on infinity; an
- *    E2M1 matrix's global scale multiplies the sum), a NaN scale makes the
- *    outputs it reaches NaN.
+ *  - Sums, bias and activation are fp32, rounded once to out_type.  silu is
+ *    within 2^-21 + |y| 2^-23 of its value, gelu within 2^-20 + y^2 2^-23 of
+ *    its own, where values below about 2^-119 may be 0.
+ *  - 4-bit weights are multiplied at their exact values (from 2^128 on
+ *    infinity; an E2M1 matrix's global scale multiplies the sum), a NaN scale
+ *    makes the outputs it reaches NaN.
  *  - A group whose matrix is outside [0, num_rows) gets rows of zeros.
  *  - Places in no group, places whose row of x is outside [0, x_rows) and
  *    places whose row of out is outside [0, out_rows) are left out: nothing is
