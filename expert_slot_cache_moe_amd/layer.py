@@ -7,10 +7,10 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (MOE_FMT_BF16, MOE_FMT_E2M1, make_pool, make_shared, moe_bank_row_bytes,
-               moe_cache_create, moe_cache_destroy, moe_layer_decode, moe_layer_decode_hybrid,
-               moe_layer_decode_router, moe_quantize_rows, moe_route, moe_routed_prefill,
-               moe_routed_prefill_workspace_bytes, moe_shared_prefill,
+from . import (MOE_FMT_BF16, MOE_FMT_E2M1, MOE_TYPE_BF16, _on_current_device, _rows_of, _type_of, _want, make_pool,
+               make_shared, moe_bank_row_bytes, moe_cache_create, moe_cache_destroy, moe_last_error,
+               moe_layer_decode, moe_layer_decode_hybrid, moe_layer_decode_router, moe_quantize_rows, moe_route,
+               moe_routed_prefill, moe_routed_prefill_workspace_bytes, moe_shared_prefill,
                moe_shared_prefill_workspace_bytes, moe_topk)
 
 
@@ -126,32 +126,48 @@ class SlotCacheLayers:
         stream: the routes of decode(), the shared expert, and
         moe_routed_prefill over `pool` (streamed_pool(layer), copied here if
         not given, which a capture cannot hold).  The cache and its statistics
-        stay as they are; any number of tokens up to 65535."""
+        stay as they are; any number of tokens up to 65535.  x and out are
+        bf16 [T, H], logits fp32 [T, E] (rows may be strided if the layer has a
+        router), ids_out int32 and w_out fp32 [T, K]; all of that, the sizes
+        and the pool's are checked before anything is launched."""
         if not 0 <= layer < self.L:
             raise ValueError(f"layer {layer} outside [0, {self.L})")
         T = x.shape[0]
-        for name, t, shape in (("x", x, (T, self.H)), ("logits", logits, (T, self.E)), ("out", out, (T, self.H)),
-                               ("ids_out", ids_out, (T, K)), ("w_out", w_out, (T, K))):
-            if t is not None and tuple(t.shape) != shape:
-                raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-        for name, t, dtype in (("logits", logits, torch.float32), ("ids_out", ids_out, torch.int32),
-                               ("w_out", w_out, torch.float32)):
-            if t is not None and t.dtype != dtype:
-                raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
+        _on_current_device(x, logits, out, ids_out, w_out)
+        router = self.routers[layer]
+        for name, t, shape, dtype in (("x", x, (T, self.H), None), ("logits", logits, (T, self.E), torch.float32),
+                                      ("out", out, (T, self.H), None), ("ids_out", ids_out, (T, K), torch.int32),
+                                      ("w_out", w_out, (T, K), torch.float32)):
+            if t is None:
+                continue
+            if t is logits and router is not None:      # a router takes rows of any stride
+                _rows_of(t, name)
+                if tuple(t.shape) != shape or t.dtype != dtype:
+                    raise ValueError(f"{name}: expected {dtype} of shape {shape}, got {t.dtype} of {tuple(t.shape)}")
+                continue
+            _want(t, name, shape, dtype)
+            if dtype is None and _type_of(t, name) != MOE_TYPE_BF16:
+                raise ValueError(f"{name} must be bfloat16")
+        if pool is not None and pool.hidden != self.H:
+            raise ValueError(f"pool: hidden {pool.hidden}, expected {self.H}")
+        n = moe_routed_prefill_workspace_bytes(
+            *((self.fmt, self.E, self.H, self.F) if pool is None else
+              (pool.weight_format, pool.num_rows, pool.hidden, pool.ffn)), T, K)
+        if n == 0:      # sizes that moe_routed_prefill would refuse
+            raise ValueError(f"a prompt of {T} tokens, top {K}: {moe_last_error()}")
         ids = torch.empty((T, K), dtype=torch.int32, device=self.device) if ids_out is None else ids_out
         w = torch.empty((T, K), dtype=torch.float32, device=self.device) if w_out is None else w_out
-        if self.routers[layer] is None:
+        if router is None:
             moe_topk(logits, K, ids, w)
         else:
-            moe_route(self.routers[layer], logits, K, ids, w)
+            moe_route(router, logits, K, ids, w)
         shared, addend = self._shared(layer), None
         if shared is not None:
             addend = torch.empty((T, self.H), dtype=torch.float32, device=self.device)
-            n = moe_shared_prefill_workspace_bytes(self.H, shared.ffn, T)
-            moe_shared_prefill(shared, self.H, x, addend, torch.empty(n, dtype=torch.uint8, device=self.device))
+            ns = moe_shared_prefill_workspace_bytes(self.H, shared.ffn, T)
+            moe_shared_prefill(shared, self.H, x, addend, torch.empty(ns, dtype=torch.uint8, device=self.device))
         if pool is None:
             pool = self.streamed_pool(layer)
-        n = moe_routed_prefill_workspace_bytes(self.fmt, pool.num_rows, self.H, self.F, T, K)
         moe_routed_prefill(pool, x, ids, w, out, torch.empty(n, dtype=torch.uint8, device=self.device),
                            addend=addend)
 
