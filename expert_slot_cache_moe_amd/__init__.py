@@ -702,7 +702,7 @@ def moe_group_routes(idx, num_rows: int, offsets, order, workspace=None, stream=
 def _product_rows(bank, x, out, activation):
     """(device, rows of x, their stride, rows of out, their stride, out type), everything checked."""
     dev = _on_current_device(x, out)
-    if bank._device != dev:
+    if getattr(bank, "_device", dev) != dev:     # (a bank filled by hand says nothing)
         _on_current_device(*bank._keep)
     x_shape, out_shape = x.shape, out.shape
     if len(x_shape) != 2 or len(out_shape) != 2:

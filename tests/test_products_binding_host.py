@@ -1,0 +1,47 @@
+"""What the binding of the products and the lists checks by itself.  No GPU:
+tensors in host memory stand for the device's, and calls that would launch
+have no rows."""
+import pytest
+import torch
+
+import expert_slot_cache_moe_amd as m
+
+P = 1 << 20      # stands for a device pointer; never followed
+
+
+@pytest.fixture
+def checked(monkeypatch):
+    """The tensors whose device was checked."""
+    seen = []
+
+    def on_current_device(*tensors):
+        m._load_torch()
+        seen.extend(t for t in tensors if t is not None)
+        return -1                                   # what get_device() says of host memory
+
+    monkeypatch.setattr(m, "_on_current_device", on_current_device)
+    monkeypatch.setattr(m, "_stream_on", lambda dev, stream: None)
+    monkeypatch.setattr(m, "_dev_ptr", lambda t: None if t is None else P)
+    return seen
+
+
+def _by_hand(num_rows=1, n=32, k=64):
+    """A bank whose fields a program has filled itself, as C's callers do."""
+    b = m.moe_bank_t()
+    b.weight_format, b.num_rows, b.n, b.k, b.weights_dev = m.MOE_FMT_BF16, num_rows, n, k, P
+    return b
+
+
+def test_a_bank_filled_by_hand_is_taken(checked):
+    x, out = torch.zeros((0, 64), dtype=torch.bfloat16), torch.zeros((0, 32))
+    m.moe_linear(_by_hand(), x, out)
+    m.moe_grouped_product(_by_hand(4), x, torch.zeros(5, dtype=torch.int32), out)
+
+
+def test_a_banks_tensors_are_checked_where_it_has_them(checked):
+    w = torch.zeros((1, 32, 64), dtype=torch.bfloat16)
+    bank = m.make_bank(m.MOE_FMT_BF16, w)
+    checked.clear()
+    bank._device = 1                                # made on another device
+    m.moe_linear(bank, torch.zeros((0, 64), dtype=torch.bfloat16), torch.zeros((0, 32)))
+    assert any(t is w for t in checked)
