@@ -798,10 +798,15 @@ def moe_routed_prefill_workspace_bytes(weight_format: int, num_rows: int, hidden
     return int(lib().moe_routed_prefill_workspace_bytes(weight_format, num_rows, hidden, ffn, T, K))
 
 
+def _weights_of(owner):
+    """The tensors that make_pool or make_shared was given (addresses aside); none for one filled by hand."""
+    return [t for t in getattr(owner, "_keep", ()) if t is not None and not isinstance(t, int)]
+
+
 def moe_routed_prefill(pool: moe_pool_t, x, idx, w, out, workspace, addend=None, stream=None) -> None:
     """moe_routed_decode for prompts of up to 2^22 routes."""
     T, K = idx.shape
-    dev = _on_current_device(x, idx, w, out, workspace, addend)
+    dev = _on_current_device(x, idx, w, out, workspace, addend, *_weights_of(pool))
     if _type_of(x, "x") != MOE_TYPE_BF16 or _type_of(out, "out") != MOE_TYPE_BF16:
         raise ValueError("x and out must be bfloat16")
     _want(x, "x", (T, pool.hidden))
@@ -822,7 +827,7 @@ def moe_shared_prefill_workspace_bytes(hidden: int, ffn: int, T: int) -> int:
 def moe_shared_prefill(shared: moe_shared_t, hidden: int, x, addend, workspace, stream=None) -> None:
     """moe_shared_expert for prompts."""
     T = x.shape[0]
-    dev = _on_current_device(x, addend, workspace)
+    dev = _on_current_device(x, addend, workspace, *_weights_of(shared))
     if _type_of(x, "x") != MOE_TYPE_BF16:
         raise ValueError("x must be bfloat16")
     _want(x, "x", (T, hidden))

@@ -7,8 +7,8 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (MOE_FMT_BF16, MOE_FMT_E2M1, MOE_TYPE_BF16, _on_current_device, _rows_of, _type_of, _want, make_pool,
-               make_shared, moe_bank_row_bytes, moe_cache_create, moe_cache_destroy, moe_last_error,
+from . import (MOE_FMT_BF16, MOE_FMT_E2M1, MOE_TYPE_BF16, _on_current_device, _rows_of, _type_of, _want, _weights_of,
+               make_pool, make_shared, moe_bank_row_bytes, moe_cache_create, moe_cache_destroy, moe_last_error,
                moe_layer_decode, moe_layer_decode_hybrid, moe_layer_decode_router, moe_quantize_rows, moe_route,
                moe_routed_prefill, moe_routed_prefill_workspace_bytes, moe_shared_prefill,
                moe_shared_prefill_workspace_bytes, moe_topk)
@@ -133,7 +133,8 @@ class SlotCacheLayers:
         if not 0 <= layer < self.L:
             raise ValueError(f"layer {layer} outside [0, {self.L})")
         T = x.shape[0]
-        _on_current_device(x, logits, out, ids_out, w_out)
+        _on_current_device(x, logits, out, ids_out, w_out, *_weights_of(self._shared(layer)),
+                           *(self.slot_banks if pool is None else _weights_of(pool)))
         router = self.routers[layer]
         for name, t, shape, dtype in (("x", x, (T, self.H), None), ("logits", logits, (T, self.E), torch.float32),
                                       ("out", out, (T, self.H), None), ("ids_out", ids_out, (T, K), torch.int32),
@@ -155,20 +156,20 @@ class SlotCacheLayers:
               (pool.weight_format, pool.num_rows, pool.hidden, pool.ffn)), T, K)
         if n == 0:      # sizes that moe_routed_prefill would refuse
             raise ValueError(f"a prompt of {T} tokens, top {K}: {moe_last_error()}")
-        ids = torch.empty((T, K), dtype=torch.int32, device=self.device) if ids_out is None else ids_out
-        w = torch.empty((T, K), dtype=torch.float32, device=self.device) if w_out is None else w_out
+        ids = torch.empty((T, K), dtype=torch.int32, device=x.device) if ids_out is None else ids_out
+        w = torch.empty((T, K), dtype=torch.float32, device=x.device) if w_out is None else w_out
         if router is None:
             moe_topk(logits, K, ids, w)
         else:
             moe_route(router, logits, K, ids, w)
         shared, addend = self._shared(layer), None
         if shared is not None:
-            addend = torch.empty((T, self.H), dtype=torch.float32, device=self.device)
+            addend = torch.empty((T, self.H), dtype=torch.float32, device=x.device)
             ns = moe_shared_prefill_workspace_bytes(self.H, shared.ffn, T)
-            moe_shared_prefill(shared, self.H, x, addend, torch.empty(ns, dtype=torch.uint8, device=self.device))
+            moe_shared_prefill(shared, self.H, x, addend, torch.empty(ns, dtype=torch.uint8, device=x.device))
         if pool is None:
             pool = self.streamed_pool(layer)
-        moe_routed_prefill(pool, x, ids, w, out, torch.empty(n, dtype=torch.uint8, device=self.device),
+        moe_routed_prefill(pool, x, ids, w, out, torch.empty(n, dtype=torch.uint8, device=x.device),
                            addend=addend)
 
     def streamed_pool(self, layer):

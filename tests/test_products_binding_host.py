@@ -45,3 +45,26 @@ def test_a_banks_tensors_are_checked_where_it_has_them(checked):
     bank._device = 1                                # made on another device
     m.moe_linear(bank, torch.zeros((0, 64), dtype=torch.bfloat16), torch.zeros((0, 32)))
     assert any(t is w for t in checked)
+
+
+def _pool(banks):
+    return m.make_pool(m.MOE_FMT_BF16, 64, 32, 4, banks)
+
+
+def test_the_device_of_a_prompts_weights_is_checked(checked):
+    """moe_routed_prefill's pool, moe_shared_prefill's matrices; addresses and what is filled by hand say nothing."""
+    x, out = torch.zeros((0, 64), dtype=torch.bfloat16), torch.zeros((0, 64), dtype=torch.bfloat16)
+    idx, w = torch.zeros((0, 2), dtype=torch.int32), torch.zeros((0, 2))
+    ws = torch.zeros(m.moe_routed_prefill_workspace_bytes(m.MOE_FMT_BF16, 4, 64, 32, 0, 2), dtype=torch.uint8)
+    banks = [torch.zeros((4, 8), dtype=torch.uint8) for _ in range(2)]
+    m.moe_routed_prefill(_pool(banks), x, idx, w, out, ws)
+    assert all(any(t is b for t in checked) for b in banks)
+    m.moe_routed_prefill(_pool([P, banks[1]]), x, idx, w, out, ws)
+    by_hand = m.moe_pool_t()
+    by_hand.weight_format, by_hand.hidden, by_hand.ffn, by_hand.num_rows = m.MOE_FMT_BF16, 64, 32, 4
+    by_hand.banks_dev[0] = by_hand.banks_dev[1] = P
+    m.moe_routed_prefill(by_hand, x, idx, w, out, ws)
+    checked.clear()
+    parts = [torch.zeros(8, dtype=torch.int16) for _ in range(3)]
+    m.moe_shared_prefill(m.make_shared(*parts, ffn=32), 64, x, torch.zeros((0, 64)), ws)
+    assert all(any(t is b for t in checked) for b in parts)
