@@ -476,6 +476,13 @@ def _stream_on(dev, stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _fits(*counts):
+    """Counts go to the library in 32 bits, and ctypes would cut longer ones to their low bits."""
+    for n in counts:
+        if n >> 31:
+            raise ValueError(f"{n}: a count has to fit in 31 bits")
+
+
 def _want(t, what, shape, dtype=None):
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous tensor of shape {shape}, got {tuple(t.shape)}"
@@ -651,6 +658,7 @@ def make_bank(fmt: int, weights, scales=None, globals=None) -> moe_bank_t:
     if weights.dim() != 3:
         raise ValueError("weights: expected [num_rows, n, k] (4-bit codes: k/2)")
     P, n, w = weights.shape
+    _fits(P, n, 2 * w)
     _on_current_device(weights, scales, globals)
     b = moe_bank_t()
     b.weight_format, b.num_rows, b.n = fmt, P, n
@@ -686,6 +694,7 @@ def moe_group_routes(idx, num_rows: int, offsets, order, workspace=None, stream=
     if idx.dim() != 2:
         raise ValueError("idx: expected [T, K]")
     T, K = idx.shape
+    _fits(T, K, num_rows)
     dev = _on_current_device(idx, offsets, order, workspace)
     _want(idx, "idx", (T, K), _I32)
     _want(offsets, "offsets", (num_rows + 1,), _I32)
@@ -709,6 +718,8 @@ def _product_rows(bank, x, out, activation):
         raise ValueError("x and out: expected 2-d tensors")
     x_rows, k = x_shape
     out_rows, cols = out_shape
+    if (x_rows | out_rows) >> 31:
+        _fits(x_rows, out_rows)
     x_stride, x_step = x.stride()
     out_stride, out_step = out.stride()
     if (x_step != 1 and k > 1) or (out_step != 1 and cols > 1):
@@ -735,6 +746,8 @@ def _bias_of(bias, shape, dev):
 
 
 def _indices(t, what, n, dev):
+    if n >> 31:
+        _fits(n)
     if t.get_device() != dev:
         _on_current_device(t)
     _want(t, what, (n,), _I32)
@@ -750,6 +763,7 @@ def moe_grouped_product(bank: moe_bank_t, x, offsets, out, matrices=None, gather
     dev, x_rows, x_stride, out_rows, out_stride, out_type = _product_rows(bank, x, out, activation)
     R = x_rows
     if gather is not None:
+        _fits(gather_div)
         R = gather.numel()
         gather = _indices(gather, "gather", R, dev)
         if scatter is not None:
@@ -806,6 +820,7 @@ def _weights_of(owner):
 def moe_routed_prefill(pool: moe_pool_t, x, idx, w, out, workspace, addend=None, stream=None) -> None:
     """moe_routed_decode for prompts of up to 2^22 routes."""
     T, K = idx.shape
+    _fits(T, K)
     dev = _on_current_device(x, idx, w, out, workspace, addend, *_weights_of(pool))
     if _type_of(x, "x") != MOE_TYPE_BF16 or _type_of(out, "out") != MOE_TYPE_BF16:
         raise ValueError("x and out must be bfloat16")
@@ -827,6 +842,7 @@ def moe_shared_prefill_workspace_bytes(hidden: int, ffn: int, T: int) -> int:
 def moe_shared_prefill(shared: moe_shared_t, hidden: int, x, addend, workspace, stream=None) -> None:
     """moe_shared_expert for prompts."""
     T = x.shape[0]
+    _fits(T, hidden)
     dev = _on_current_device(x, addend, workspace, *_weights_of(shared))
     if _type_of(x, "x") != MOE_TYPE_BF16:
         raise ValueError("x must be bfloat16")

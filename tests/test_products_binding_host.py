@@ -68,3 +68,38 @@ def test_the_device_of_a_prompts_weights_is_checked(checked):
     parts = [torch.zeros(8, dtype=torch.int16) for _ in range(3)]
     m.moe_shared_prefill(m.make_shared(*parts, ffn=32), 64, x, torch.zeros((0, 64)), ws)
     assert all(any(t is b for t in checked) for b in parts)
+
+
+MANY = (1 << 32) + 5          # 5 to a call that takes 32 bits
+
+
+def _many(cols, dtype=torch.bfloat16):
+    """A tensor of 2^32 + 5 rows without memory."""
+    return torch.empty((MANY, cols), dtype=dtype, device="meta")
+
+
+def test_more_rows_than_a_call_can_count_are_refused(checked):
+    """Counts go to the library in 32 bits: a longer one is refused, not cut to its low bits."""
+    i32 = torch.int32
+    x, out, off = torch.zeros((8, 64), dtype=torch.bfloat16), torch.zeros((8, 32)), torch.zeros(2, dtype=i32)
+    bank = _by_hand()
+    idx = torch.zeros((8, 2), dtype=i32)
+    refused = [
+        lambda: m.moe_linear(bank, _many(64), _many(32)),
+        lambda: m.moe_grouped_product(bank, _many(64), off, out, gather=torch.zeros(8, dtype=i32)),
+        lambda: m.moe_grouped_product(bank, x, off, _many(32), scatter=torch.zeros(8, dtype=i32)),
+        lambda: m.moe_grouped_product(bank, x, off, out, gather=_many(1, i32).view(-1)),
+        lambda: m.moe_grouped_product(bank, x, off, out, scatter=_many(1, i32).view(-1)),
+        lambda: m.moe_grouped_product(bank, x, _many(1, i32).view(-1), out, matrices=_many(1, i32).view(-1)[:-1]),
+        lambda: m.moe_grouped_product(bank, x, off, out, gather=torch.zeros(8, dtype=i32), gather_div=(1 << 32) + 1),
+        lambda: m.moe_group_routes(_many(1, i32), 4, torch.zeros(5, dtype=i32), _many(1, i32).view(-1)),
+        lambda: m.moe_routed_prefill(_pool([]), _many(64), _many(2, i32), _many(2, torch.float32), _many(64), x),
+        lambda: m.moe_shared_prefill(m.make_shared(None, None, None, ffn=32), 64, _many(64), _many(64, torch.float32), x),
+        lambda: m.make_bank(m.MOE_FMT_BF16, torch.empty((1, MANY, 2), dtype=torch.bfloat16, device="meta")),
+    ]
+    for i, call in enumerate(refused):
+        with pytest.raises(ValueError, match="31 bits"):
+            call()
+            pytest.fail(f"call {i} was taken")
+    with pytest.raises((ValueError, m.MoeError)):
+        m.moe_group_routes(idx, (1 << 32) + 4, torch.zeros(5, dtype=i32), torch.zeros(16, dtype=i32))
