@@ -618,7 +618,8 @@ moe_status_t moe_group_routes(const int32_t *idx_dev, int32_t T, int32_t K, int3
  *    places whose row of out is outside [0, out_rows) are left out: nothing is
  *    written for them.  Rows of out that no place names stay as they were.
  *  - offsets ascend from at least 0 to at most R (others are cut to that
- *    range); two places must not name one row of out.
+ *    range); two places must not name one row of out.  out must not overlap
+ *    anything that the call reads.
  * Within a call a place's result depends on its matrix (its bytes, and its
  * number in the bank) and its x alone; calls of other sizes may add in another
  * order.
@@ -644,7 +645,8 @@ moe_status_t moe_grouped_product(const moe_bank_t *bank, const void *x_dev, int6
  *   out[t] = act(W x_t + bias) + residual[t].
  * residual_dev: [T] rows of out's columns, of residual_type,
  * residual_stride elements apart, or NULL; it may be out itself (same type and
- * stride).  Everything else as moe_grouped_product. */
+ * stride), and overlap it in no other way.  Everything else as
+ * moe_grouped_product. */
 moe_status_t moe_linear(const moe_bank_t *bank, const void *x_dev, int64_t x_stride, int32_t T,
                         int32_t activation, int32_t bias_type, const void *bias_dev,
                         int32_t residual_type, const void *residual_dev, int64_t residual_stride,
