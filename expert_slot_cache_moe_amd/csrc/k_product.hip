@@ -19,17 +19,24 @@ int64_t even_blocks(const ProductParams &p, int form) {
 // a tile passes all of k stage by stage (dense bf16, us, split / 32 places:
 // 256 blocks of k 2048 6.2 / 12.0, 512 10.3 / 14.4, 1024 18.7 / 14.6; 512 of k
 // 4096 17.8 / 25.3, 1024 33.2 / 26.2; 1024 of k 1024 11.6 / 10.3, 2048 21.1 /
-// 12.2).  With rows of x that are no whole vectors of eight fewer (k 1061, 128
-// blocks 9.2 / 9.5, 512 16.5 / 9.7), with 4-bit weights more (MXFP4, k 1056,
-// 528 blocks 8.2 / 10.0; k 1024, 1024 blocks 9.2 / 8.7).
-constexpr int64_t kSplitBlocks = 512, kSplitBlocksCut = 192, kSplitBlocksCodes = 800;
+// 12.2).  With rows of x that are no whole vectors of eight only one for each
+// CU (k 203, 256 blocks 4.6 / 5.4, 320 7.0 / 5.4; k 1061, 192 and 256 8.4 /
+// 9.8, 320 14.6 / 9.8; k 2051, 256 12.5 / 15.4, 320 22.7 / 15.3; grouped, 515
+// columns of k 1061, 198 8.9 / 12.7, 264 13.8 / 12.7), with 4-bit weights
+// more (E2M1 and MXFP4, k 1024, 768 blocks 7.4 / 9.2 and 7.3 / 8.4, 832 8.6 /
+// 9.1 and 8.5 / 8.4; k 2048, 768 11.7 / 15.2 and 11.4 / 13.3, 832 14.1 / 15.0
+// and 13.9 / 13.4; k 1024, 1280 10.6 / 9.3 and 10.3 / 8.4).
+constexpr int64_t kSplitBlocks = 512, kSplitBlocksCut = 256, kSplitBlocksCodes = 800;
 // The mean places of a matrix from which a tile of 64, 128, 256 places pays
 // (bf16, 64 matrices of 2048 x 2048, us at 32 / 64 / 128 / 256 places: mean 8
 // 96 96 95 132, 16 103 97 96 128, 48 156 107 115 134, 64 195 117 116 136, 96
 // 261 153 126 187, 192 444 253 176 197, 256 578 326 224 201; 160 of 512 x
 // 1024: mean 8 27 28 34 64, 16 29 30 34 64, 64 64 40 41 66, 96 80 55 44 67,
-// 256 161 110 82 79), and for 4 bits one of 64 (E2M1, 64 of 2048 x 2048, 32 /
-// 64 places: mean 32 52 60, 48 67 63, 96 117 98).
+// 256 161 110 82 79; between 6 and 24 places 32 and 64 are within 4 % of each
+// other where the groups are alike, and 64 is up to 15 % faster where some are
+// longer: popular rows, 96 of 1024 x 2048, mean 8 83 72, 12 84 74, 16 84 84),
+// and for 4 bits one of 64 (E2M1, 64 of 2048 x 2048, 32 / 64 places: mean 32
+// 52 60, 48 67 63, 96 117 98).
 constexpr int64_t kMean64 = 12, kMean128 = 72, kMean256 = 224, kMeanCodes64 = 40;
 // A larger tile is taken only where there is a block for each of the 256 CUs
 // (dense 4096 x 4096, us at 64 / 128 / 256 places: 512 rows 41 41 92, 1024 56
